@@ -8,7 +8,9 @@ Importing this package loads libsplitzip.so and raises ImportError if it has not
 been built (python fp8_kv_cache_exp_b200/build.py); there is no other path.
 """
 import ctypes
+import math
 import os
+import struct
 
 import torch
 
@@ -22,6 +24,8 @@ __all__ = [
     "sz_decode",
     "sz_decode_batched", "sz_last_device_status", "sz_encode_noalloc", "dtype_of", "elem_bytes", "numel_of",
     "new_workspace", "new_plans", "Batch",
+    "KVCache", "sz_ops_workspace_bytes", "new_ops_workspace", "rope_table", "sz_kv_append_paged", "sz_qk_norm_rope",
+    "sz_attn_paged",
 ]
 
 SZ_BF16 = 0
@@ -85,6 +89,10 @@ def _load():
         "sz_last_device_status": (i32, [vp, vp]),
         "sz_enable_peer_access": (i32, [i32, i32]),
         "sz_encode_noalloc": (i32, [i32, vp, vp, u64, vp, sz, vp, vp]),
+        "sz_ops_workspace_bytes": (sz, [vp]),
+        "sz_kv_append_paged": (i32, [vp, vp, vp, sz, vp]),
+        "sz_qk_norm_rope": (i32, [vp, vp, sz, vp]),
+        "sz_attn_paged": (i32, [vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -453,3 +461,214 @@ def sz_encode_noalloc(dtype: int, plan: torch.Tensor, x: torch.Tensor, out: torc
     _check(lib.sz_encode_noalloc(dtype, _p(plan), _p(x), numel_of(x, dtype), _p(out), out.nbytes,
                                  _p(status) if status is not None else None, _stream(stream)),
            "sz_encode_noalloc")
+
+
+# ------------------------------------------------ operators on a paged cache
+#
+# The argument structs of include/splitzip.h are packed by `struct` with native
+# alignment and handed over as bytes: one call's structs belong to that call
+# alone, so calls from several threads do not share them.
+
+_CACHE = struct.Struct("@3Q2Q8I")                         # sz_kv_cache_t
+_APPEND = struct.Struct("@Q" + "3Q2I" * 4 + "2Q" + "2QfI" + "2Q4I")   # sz_kv_append_t
+_NORM_ROPE = struct.Struct("@Q" + "3Q2I" * 4 + "2QfI" + "2Q4I" + "2I")  # sz_qk_norm_rope_t
+_ATTN = struct.Struct("@Q" + "3Q2I" * 2 + "3Q" + "f3I")   # sz_attn_t
+_NO_HEADS = (0, 0, 0, 0, 0)
+
+
+class KVCache:
+    """A paged KV cache: k_pool and v_pool [pages, page_tokens, kv_heads, head_dim], bfloat16 or
+    float8_e5m2, contiguous inside a page and with the same stride from page to page; table [seqs,
+    table_pages] int32, a row the page ids of one sequence in token order.  A row is also the `pages`
+    of paged() with page_elems = page_tokens * kv_heads * head_dim, so a sequence can be coded where it
+    lies.  The tensors must stay alive and in place while the cache is in use (the object holds them);
+    their contents may change between calls."""
+
+    def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor, table: torch.Tensor):
+        self.dtype = dtype_of(k_pool)
+        if v_pool.dtype != k_pool.dtype or v_pool.shape != k_pool.shape or k_pool.dim() != 4:
+            raise ValueError("k_pool and v_pool: [pages, page_tokens, kv_heads, head_dim], of one shape and dtype")
+        if table.dtype != torch.int32:
+            raise TypeError("page ids are int32")
+        if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table: [seqs, table_pages], rows contiguous")
+        if not (k_pool.device == v_pool.device == table.device):
+            raise ValueError("the pools and the table must be on one device")
+        pages, tokens, heads, dim = k_pool.shape
+        run = tokens * heads * dim
+        for x in (k_pool, v_pool):
+            if x.numel() == 0 or not x[0].is_contiguous():
+                raise ValueError("a page must be contiguous")
+        strides = {x.stride(0) for x in (k_pool, v_pool)} if pages > 1 else {-(-run // 16) * 16}
+        if len(strides) != 1 or min(strides) < run:
+            raise ValueError("pages must not overlap and have one stride in both pools")
+        self.k_pool, self.v_pool, self.table = k_pool, v_pool, table
+        self.seqs, self.kv_heads, self.head_dim, self.page_tokens = table.shape[0], heads, dim, tokens
+        self._dev = k_pool.get_device()
+        seqs, width = table.shape
+        self._c = _CACHE.pack(k_pool.data_ptr(), v_pool.data_ptr(), table.data_ptr(), pages,
+                              strides.pop() * elem_bytes(self.dtype), table.stride(0) if seqs > 1 else width, width,
+                              seqs, tokens, heads, dim, self.dtype, 0)
+
+    def pages(self, seq: int, tokens: int):
+        """(paged() descriptors of the keys and the values, their element count) of a sequence's first
+        `tokens` tokens, for the paged calls of the codec."""
+        pe = self.page_tokens * self.kv_heads * self.head_dim
+        out = []
+        for pool in (self.k_pool, self.v_pool):
+            d = sz_paged_t(pool.data_ptr(), self.table[seq].data_ptr(), pool.shape[0],
+                           (pool.stride(0) if pool.shape[0] > 1 else pe) * elem_bytes(self.dtype), pe)
+            d._refs = (pool, self.table)
+            out.append(d)
+        return out, int(tokens) * self.kv_heads * self.head_dim
+
+
+def sz_ops_workspace_bytes(cache: KVCache = None) -> int:
+    return int(lib.sz_ops_workspace_bytes(None if cache is None else cache._c))
+
+
+def new_ops_workspace(cache: KVCache = None, device=None, stream=None) -> torch.Tensor:
+    """A zero-initialised workspace for the operators on `cache` (without one: for sz_qk_norm_rope)."""
+    n = sz_ops_workspace_bytes(cache)
+    if n == 0:
+        raise SplitZipError(SZ_ERR_INVALID_ARG, "sz_ops_workspace_bytes")
+    if device is None:
+        device = "cuda" if cache is None else cache.k_pool.device
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        sz_workspace_init(ws, stream)
+    return ws
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """[positions, rot] float32: the cosines of position p's angles p * base^(-2i/rot), then their sines,
+    from angles in 64 bits."""
+    inv = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def _on(dev: int, *tensors):
+    """Every tensor is on CUDA device `dev`, and that is the current device."""
+    for x in tensors:
+        if x is not None and x.get_device() != dev:
+            raise ValueError("all tensors must be on the cache's device (the first tensor's)")
+    if dev < 0 or torch.cuda.current_device() != dev:
+        raise ValueError("the tensors' CUDA device must be the current device")
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _heads(x: torch.Tensor, dim: int, name: str):
+    """sz_heads_t of a bfloat16 view [tokens, heads, dim] whose rows are contiguous."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError("%s: bfloat16" % name)
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError("%s: [tokens, heads, %d]" % (name, dim))
+    ts, hs, es = x.stride()
+    if es != 1:
+        raise ValueError("%s: a head's elements must be contiguous" % name)
+    return x.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0, shape[1], 0
+
+
+def _vector(x, dtype, n, name):
+    """Device pointer of a contiguous vector of n elements (0 for None)."""
+    if x is None:
+        return 0
+    if x.dtype != dtype:
+        raise TypeError("%s: %s" % (name, dtype))
+    if x.numel() != n or not x.is_contiguous():
+        raise ValueError("%s: %d contiguous elements" % (name, n))
+    return x.data_ptr()
+
+
+def _norm_rope_args(dim, tokens, q_norm, k_norm, eps, rope, positions, interleaved):
+    norm = (_vector(q_norm, torch.bfloat16, dim, "q_norm"), _vector(k_norm, torch.bfloat16, dim, "k_norm"),
+            eps, 0)
+    if rope is None:
+        return norm + (0, 0, 0, 0, 0, 0)
+    if rope.dim() != 2:
+        raise ValueError("rope: [positions, rot]")
+    n, rot = rope.shape
+    return norm + (_vector(rope, torch.float32, n * rot, "rope"),
+                   _vector(positions, torch.int32, tokens, "positions"), n, rot, 1 if interleaved else 0, 0)
+
+
+def sz_kv_append_paged(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor,
+                       ws: torch.Tensor, q: torch.Tensor = None, q_out: torch.Tensor = None,
+                       q_norm: torch.Tensor = None, k_norm: torch.Tensor = None, eps: float = 1e-6,
+                       rope: torch.Tensor = None, positions: torch.Tensor = None, interleaved: bool = False,
+                       stream=None):
+    """Write new tokens' keys (normalised by k_norm, rotated by rope) and values into the cache, and the
+    queries, normalised and rotated, to q_out (default: in place).
+
+    k, v: [tokens, kv_heads, head_dim] bfloat16 views; q, q_out: [tokens, heads, head_dim].  Rows
+    cu_q[s]:cu_q[s+1] are the last tokens of sequence s, whose length with them is kv_len[s] (int32 device
+    tensors); rows behind cu_q[-1] are left alone.  q_norm, k_norm: bfloat16 [head_dim]; rope: float32
+    [positions, rot], see rope_table; positions: int32 [tokens], default each token's place."""
+    dim, tokens = cache.head_dim, k.shape[0]
+    _on(cache._dev, k, v, cu_q, kv_len, ws, q, q_out, q_norm, k_norm, rope, positions)
+    if v.shape[0] != tokens or (q is not None and q.shape[0] != tokens):
+        raise ValueError("k, v and q must have the same number of tokens")
+    qh = oh = _NO_HEADS
+    if q is not None:
+        qh = _heads(q, dim, "q")
+        oh = qh if q_out is None else _heads(q_out, dim, "q_out")
+        if q_out is not None and q_out.shape[0] != tokens:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    args = _APPEND.pack(tokens, *_heads(k, dim, "k"), *_heads(v, dim, "v"), *qh, *oh,
+                        _vector(cu_q, torch.int32, cache.seqs + 1, "cu_q"),
+                        _vector(kv_len, torch.int32, cache.seqs, "kv_len"),
+                        *_norm_rope_args(dim, tokens, q_norm, k_norm, eps, rope, positions, interleaved))
+    _check(lib.sz_kv_append_paged(cache._c, args, _ptr(ws), ws.nbytes, _raw_stream(stream, cache._dev)),
+           "sz_kv_append_paged")
+
+
+def sz_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_out: torch.Tensor, k_out: torch.Tensor, ws: torch.Tensor,
+                    q_norm: torch.Tensor = None, k_norm: torch.Tensor = None, eps: float = 1e-6,
+                    rope: torch.Tensor = None, positions: torch.Tensor = None, interleaved: bool = False,
+                    stream=None):
+    """Normalise and rotate query and key heads [tokens, heads, head_dim] (bfloat16 views; q or k may be
+    None with its output).  Outputs may be the inputs themselves.  positions: int32 [tokens]."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k")
+    tokens, dim = x.shape[0], x.shape[-1]
+    _on(x.get_device(), q, k, q_out, k_out, ws, q_norm, k_norm, rope, positions)
+    views = []
+    for a, b, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if (a is None) != (b is None):
+            raise ValueError("%s and %s_out come together" % (name, name))
+        if a is None:
+            views += _NO_HEADS + _NO_HEADS
+            continue
+        if a.shape[0] != tokens or b.shape[0] != tokens:
+            raise ValueError("q, k and their outputs must have the same number of tokens")
+        views += _heads(a, dim, name) + _heads(b, dim, name + "_out")
+    args = _NORM_ROPE.pack(tokens, *views,
+                           *_norm_rope_args(dim, tokens, q_norm, k_norm, eps, rope, positions, interleaved), dim, 0)
+    _check(lib.sz_qk_norm_rope(args, _ptr(ws), ws.nbytes, _raw_stream(stream, x.get_device())), "sz_qk_norm_rope")
+
+
+def sz_attn_paged(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, out: torch.Tensor,
+                  ws: torch.Tensor, scale: float = None, causal: bool = True, window: int = 0,
+                  lse: torch.Tensor = None, stream=None):
+    """Attention of new tokens over the cache: out = softmax(scale * q k^T) v, for packed rows q, out
+    [tokens, heads, head_dim] (bfloat16 views) of the sequences that cu_q and kv_len describe (as in
+    sz_kv_append_paged; the tokens' own keys and values are in the cache).  scale: default head_dim^-0.5;
+    window: w > 0 lets a row see the last w places up to its own; lse: float32 [tokens, heads]."""
+    dim, tokens = cache.head_dim, q.shape[0]
+    _on(cache._dev, q, cu_q, kv_len, out, ws, lse)
+    if out.shape[0] != tokens:
+        raise ValueError("out must have q's shape")
+    qh = _heads(q, dim, "q")
+    args = _ATTN.pack(tokens, *qh, *_heads(out, dim, "out"), _vector(cu_q, torch.int32, cache.seqs + 1, "cu_q"),
+                      _vector(kv_len, torch.int32, cache.seqs, "kv_len"),
+                      _vector(lse, torch.float32, tokens * qh[3], "lse"),
+                      1.0 / math.sqrt(dim) if scale is None else scale, 1 if causal else 0, window, 0)
+    _check(lib.sz_attn_paged(cache._c, args, _ptr(ws), ws.nbytes, _raw_stream(stream, cache._dev)), "sz_attn_paged")

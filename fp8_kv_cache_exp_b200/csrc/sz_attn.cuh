@@ -1,0 +1,296 @@
+// sz_attn.cuh -- what the attention kernels share: how the work is cut and
+// shared out, how partial results are joined, and the exact path of a row.
+//
+// A tile is TR rows of one sequence and one KV head: a row is a (token, query
+// head of the group) pair, row r being token r / G, head r % G, so that one
+// pass over keys and values serves all query heads that share them.  A tile's
+// work is counted in blocks of BN places that any of its rows sees.  The
+// blocks of all tiles, in the order (KV head, sequence, tile, block), are dealt
+// out evenly: CTA c of C has blocks [c U / C, (c + 1) U / C).  A tile that
+// falls to several CTAs is joined from their partial results, in the order of
+// the CTAs, by the one that finishes last; so the result does not depend on
+// which one that is.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "sz_ops.cuh"
+
+namespace sz {
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct SeqInfo {
+    uint32_t q0, q_len, kv;
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttnParams &p, uint32_t b) {
+    const int32_t a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1), n = __ldg(p.kv_len + b);
+    SeqInfo s;
+    const int32_t last = int32_t(p.tokens);
+    const int32_t a1 = a < 0 ? 0 : (a > last ? last : a), e1 = e > last ? last : e;
+    s.q0 = uint32_t(a1);
+    s.q_len = e1 > a1 ? uint32_t(e1 - a1) : 0u;
+    s.kv = n < 0 ? 0u : (uint32_t(n) > p.cache.capacity ? p.cache.capacity : uint32_t(n));
+    return s;
+}
+
+// Places that a token sees: [lo, hi).
+struct Range {
+    uint32_t lo, hi;
+};
+__device__ __forceinline__ Range token_range(const AttnParams &p, const SeqInfo &s, uint32_t i) {
+    const int64_t at = int64_t(s.kv) - int64_t(s.q_len) + int64_t(i);
+    int64_t hi = p.causal ? at + 1 : int64_t(s.kv);
+    if (hi < 0) hi = 0;
+    int64_t lo = p.window ? at - int64_t(p.window) + 1 : 0;
+    if (lo < 0) lo = 0;
+    if (lo > hi) lo = hi;
+    return Range{uint32_t(lo), uint32_t(hi)};
+}
+
+// Places that any row of a tile sees.  The first token's window reaches
+// furthest back, the last token sees furthest.
+template <int TR>
+__device__ __forceinline__ Range tile_range(const AttnParams &p, const SeqInfo &s, uint32_t tile) {
+    const uint32_t rows = s.q_len * p.group.d;
+    const uint32_t r1 = min((tile + 1) * uint32_t(TR), rows) - 1;
+    const Range a = token_range(p, s, div_by(tile * TR, p.group)), b = token_range(p, s, div_by(r1, p.group));
+    return Range{a.lo < b.hi ? a.lo : b.hi, b.hi};
+}
+
+template <int BN>
+__device__ __forceinline__ uint32_t range_blocks(const Range &r) {
+    const uint32_t n = (r.hi + BN - 1) / BN - r.lo / BN;
+    return n > 0 ? n : 1;  // a tile whose rows see nothing has its zeros to write
+}
+
+template <int TR>
+__device__ __forceinline__ uint32_t seq_tiles(const AttnParams &p, const SeqInfo &s) {
+    return (s.q_len * p.group.d + TR - 1) / TR;
+}
+
+// Where a CTA stands in its share of the blocks.
+struct Work {
+    uint64_t at, end;       // next block of the share, its end (global numbers)
+    uint64_t total;         // blocks in all
+    uint32_t ctas;          // CTAs that have a share
+    uint32_t head, seq, tile;
+    uint32_t from;          // the block of the tile at which `at` stands
+};
+
+template <int NT>
+struct WorkScratch {
+    uint64_t warp[NT / 32];
+    uint64_t found_at;
+    uint32_t tp[NT], q_len[NT], kv[NT];
+    uint32_t found[3];
+};
+
+template <int NT>
+__device__ __forceinline__ uint64_t block_scan64(uint64_t v, uint64_t *s_warp, uint64_t *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    uint64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        const uint64_t s = s_warp[w];
+        before += (w < warp) ? s : 0u;
+        all += s;
+    }
+    *total = all;
+    return before + x - v;
+}
+
+// The CTA's share; false if it has none.  All NT threads call it.
+template <int NT, int TR, int BN>
+__device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w) {
+    const uint32_t tid = threadIdx.x, seqs = p.cache.seqs;
+    // this thread's tile of the chunk looked at last
+    uint32_t seq = 0, tile = 0, units = 0, chunks = 0;
+    uint64_t before = 0;
+    auto note = [&](uint64_t target) {
+        if (units > 0 && target >= before && target - before < units) {
+            s.found[0] = seq;
+            s.found[1] = tile;
+            s.found[2] = uint32_t(target - before);
+        }
+    };
+    // blocks of all tiles of one head; with `find`, notes the tile that block `target` falls in
+    auto scan = [&](bool find, uint64_t target) {
+        uint64_t run = 0;
+        for (uint32_t sb = 0; sb < seqs; sb += NT) {
+            const uint32_t b = sb + tid;
+            uint32_t tiles = 0;
+            if (b < seqs) {
+                const SeqInfo si = seq_info(p, b);
+                tiles = seq_tiles<TR>(p, si);
+                s.q_len[tid] = si.q_len;
+                s.kv[tid] = si.kv;
+                if (!find && blockIdx.x == 0 && __ldg(p.kv_len + b) > int32_t(p.cache.capacity))
+                    set_error(p.ctl, SZ_ERR_INVALID_ARG, b);
+            }
+            uint64_t count;
+            s.tp[tid] = uint32_t(block_scan64<NT>(tiles, s.warp, &count));
+            __syncthreads();
+            for (uint32_t tb = 0; tb < uint32_t(count); tb += NT) {
+                const uint32_t t = tb + tid;
+                units = 0;
+                if (t < uint32_t(count)) {
+                    uint32_t j = 0, hi = min(seqs - sb, uint32_t(NT));  // tp[j] <= t < tp[hi]
+                    while (hi - j > 1) {
+                        const uint32_t mid = (j + hi) / 2;
+                        if (s.tp[mid] <= t) j = mid; else hi = mid;
+                    }
+                    seq = sb + j;
+                    tile = t - s.tp[j];
+                    units = range_blocks<BN>(tile_range<TR>(p, SeqInfo{0, s.q_len[j], s.kv[j]}, tile));
+                }
+                uint64_t sum;
+                before = run + block_scan64<NT>(units, s.warp, &sum);
+                run += sum;
+                ++chunks;
+                if (find) note(target);
+            }
+            __syncthreads();
+        }
+        return run;
+    };
+    const uint64_t per_head = scan(false, 0);
+    w.total = per_head * p.cache.kv_heads;
+    w.ctas = w.total < gridDim.x ? uint32_t(w.total) : gridDim.x;
+    if (blockIdx.x >= w.ctas) return false;
+    w.at = w.total * blockIdx.x / w.ctas;
+    w.end = w.total * (blockIdx.x + 1) / w.ctas;
+    const uint64_t target = w.at % per_head;
+    if (chunks == 1) note(target);  // the one chunk is still at hand
+    else scan(true, target);
+    __syncthreads();
+    w.head = uint32_t(w.at / per_head);
+    w.seq = s.found[0];
+    w.tile = s.found[1];
+    w.from = s.found[2];
+    __syncthreads();
+    return true;
+}
+
+// A CTA's part of a tile: blocks [from, to) of its n.
+struct Part {
+    SeqInfo s;
+    Range r;
+    uint32_t rows, r0;      // rows of the tile, the first of them
+    uint32_t block0;        // the tile's first block
+    uint32_t from, to, n;
+    uint32_t c_first, c_last;  // CTAs that share the tile
+};
+
+template <int TR, int BN>
+__device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w) {
+    Part t;
+    t.s = seq_info(p, w.seq);
+    t.r = tile_range<TR>(p, t.s, w.tile);
+    t.r0 = w.tile * TR;
+    t.rows = min(uint32_t(TR), t.s.q_len * p.group.d - t.r0);
+    t.block0 = t.r.lo / BN;
+    t.n = range_blocks<BN>(t.r);
+    t.from = w.from;
+    t.to = uint32_t(min(uint64_t(t.n), w.from + (w.end - w.at)));
+    if (t.from == 0 && t.to == t.n) {
+        t.c_first = t.c_last = blockIdx.x;
+    } else {
+        // block x belongs to the last CTA c with floor(total c / ctas) <= x
+        const uint64_t x0 = w.at - w.from, x1 = x0 + t.n - 1;
+        t.c_first = uint32_t(((x0 + 1) * w.ctas - 1) / w.total);
+        t.c_last = uint32_t(((x1 + 1) * w.ctas - 1) / w.total);
+    }
+    return t;
+}
+
+// On to the next tile; false at the end of the share.
+template <int TR>
+__device__ __forceinline__ bool work_next(const AttnParams &p, Work &w, const Part &t) {
+    w.at += t.to - t.from;
+    if (w.at >= w.end) return false;
+    w.from = 0;
+    if (++w.tile < seq_tiles<TR>(p, t.s)) return true;
+    w.tile = 0;
+    do {
+        if (++w.seq == p.cache.seqs) {
+            w.seq = 0;
+            if (++w.head >= p.cache.kv_heads) return false;  // only if cu_q changed under the call
+        }
+    } while (seq_info(p, w.seq).q_len == 0);
+    return true;
+}
+
+// Slot of a CTA's partial result: the tile that it takes over from another
+// CTA, or the one that it leaves to the next.
+__device__ __forceinline__ uint32_t part_slot(uint32_t c, const Part &t) { return 2 * c + (c == t.c_first ? 1 : 0); }
+
+// One row by one warp, place by place over what it sees and nothing else: for
+// rows whose matrix products met infinities or NaN.  In those a place that the
+// row does not see, but another row of the tile does, has weight 0, and 0
+// times an infinity is NaN; here such a place is never touched.
+template <int DT>
+__device__ __noinline__ void attend_row(const AttnParams &p, const SeqInfo &s, uint32_t seq, uint32_t kvh, uint32_t row) {
+    const uint32_t lane = threadIdx.x & 31, d = p.cache.head_dim;
+    const uint32_t i = div_by(row, p.group), head = kvh * p.group.d + row - i * p.group.d;
+    const Range r = token_range(p, s, i);
+    const int32_t *ids = p.cache.table + uint64_t(seq) * p.cache.table_stride;
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q.p + (s.q0 + i) * p.q.ts + head * p.q.hs);
+    float qv[8], o[8], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t e = lane + 32 * j;
+        qv[j] = e < d ? __uint_as_float(uint32_t(q[e]) << 16) : 0.f;
+        o[j] = 0.f;
+    }
+    auto load = [&](const uint8_t *base, uint32_t e) {
+        if constexpr (DT == SZ_BF16)
+            return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t *>(base) + e)) << 16);
+        else
+            return __half2float(__ushort_as_half(uint16_t(uint32_t(__ldg(base + e)) << 8)));
+    };
+    for (uint32_t t = r.lo; t < r.hi; ++t) {
+        const uint64_t off = place_offset(p.cache, p.ctl, ids, t);
+        const uint64_t at = off + uint64_t(kvh) * d * (DT == SZ_BF16 ? 2 : 1);
+        float x = 0.f;
+        if (off != kBadOffset) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (lane + 32 * j < d) x = fmaf(qv[j], load(p.cache.k + at, lane + 32 * j), x);
+        }
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+        x *= p.scale_log2;
+        const float mn = fmaxf(m, x), safe = mn == -INFINITY ? 0.f : mn;
+        const float c = exp2_fast(m - safe), e = exp2_fast(x - safe);
+        m = mn;
+        l = l * c + e;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = lane + 32 * j < d && off != kBadOffset;
+            o[j] = fmaf(e, in ? load(p.cache.v + at, lane + 32 * j) : 0.f, o[j] * c);
+        }
+    }
+    uint16_t *out = reinterpret_cast<uint16_t *>(p.out.p + (s.q0 + i) * p.out.ts + head * p.out.hs);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (lane + 32 * j < d) out[lane + 32 * j] = uint16_t(pack_bf16(l == 0.f ? 0.f : o[j] / l, 0.f));
+}
+
+}  // namespace sz

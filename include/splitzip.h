@@ -321,6 +321,165 @@ sz_status sz_last_device_status(void *d_ws, cudaStream_t stream);
 sz_status sz_encode_noalloc(sz_dtype dtype, const sz_plan_t *d_plan, const void *d_in, uint64_t n,
                             void *d_out, size_t out_cap, uint32_t *d_status, cudaStream_t stream);
 
+/* ------------------------------------------------ operators on a paged cache
+ *
+ * What a serving engine does with the cache between two codings of it: write
+ * new tokens' keys and values into its pages (sz_kv_append_paged), attend to
+ * them (sz_attn_paged), and, for caches that are kept contiguous, normalise
+ * and rotate queries and keys (sz_qk_norm_rope).  The pages are those of
+ * sz_paged_t: a row of `table` is a descriptor's `pages`, and its page_elems is
+ * page_tokens * kv_heads * head_dim, so a sequence's keys or values can be
+ * coded where they lie.
+ *
+ * Queries, keys, values and outputs are BF16; the cache is BF16 or E5M2.
+ * Arithmetic is in 32 bits, rounded once to the type that is written (to
+ * nearest, ties to even; beyond E5M2's range that is infinity, as in torch's
+ * conversion).  The conventions at the top of this file hold here too; the
+ * structs below are host data, read during the call.  d_ws is sized by
+ * sz_ops_workspace_bytes and zeroed once by sz_workspace_init; it may be shared
+ * with the codec's calls on the same stream if it is large enough for both. */
+
+/* A paged cache of `seqs` sequences.  Token t of sequence s has its key (all
+ * heads) at
+ *     k_pool + table[s * table_stride + t / page_tokens] * page_bytes
+ *            + (t % page_tokens) * kv_heads * head_dim * element bytes
+ * and its value at the same place of v_pool.
+ *   k_pool, v_pool  device, 16-byte aligned, one dtype
+ *   table           device int32, seqs rows of table_pages ids; an id outside
+ *                   [0, pool_pages) is reported as SZ_ERR_INVALID_ARG on the
+ *                   device error word where a token of that page is needed,
+ *                   and the page is neither read nor written
+ *   page_bytes      bytes from one page to the next in either pool, a
+ *                   multiple of 16, at least page_tokens * kv_heads * head_dim
+ *                   * element bytes
+ *   head_dim        a multiple of 16, 16..256
+ * page_tokens is 1..2^20, table_pages * page_tokens below 2^31, seqs 1..65536. */
+typedef struct {
+    void *k_pool;
+    void *v_pool;
+    const int32_t *table;
+    uint64_t pool_pages;
+    uint64_t page_bytes;
+    uint32_t table_stride;
+    uint32_t table_pages;
+    uint32_t seqs;
+    uint32_t page_tokens;
+    uint32_t kv_heads;
+    uint32_t head_dim;
+    uint32_t dtype; /* sz_dtype */
+    uint32_t reserved;
+} sz_kv_cache_t;
+
+/* BF16 activations [tokens, heads, head_dim]: element (t, h, i) at
+ * data + 2 * (t * token_stride + h * head_stride + i).  data is 16-byte
+ * aligned, both strides are multiples of 8 (an input may repeat rows with
+ * stride 0; rows of an output must not overlap).  data NULL: absent, where
+ * the call allows it. */
+typedef struct {
+    void *data;
+    uint64_t token_stride;
+    uint64_t head_stride;
+    uint32_t heads;
+    uint32_t reserved;
+} sz_heads_t;
+
+/* Root-mean-square norm of each head before the rotation:
+ *     x_i * weight_i / sqrt(mean(x^2) + eps)
+ * weights BF16 [head_dim], 16-byte aligned, NULL: no norm.  eps >= 0. */
+typedef struct {
+    const void *q_weight;
+    const void *k_weight;
+    float eps;
+    uint32_t reserved;
+} sz_head_norm_t;
+
+/* Rotation of a head's first `rot` elements by its position's angles.  table:
+ * device float [table_len, rot], 16-byte aligned: rot/2 cosines, then rot/2
+ * sines; NULL: no rotation.  rot is a multiple of 8, at most head_dim.  Pairs
+ * are (i, i + rot/2), or (2i, 2i + 1) where `interleaved` is not 0.  positions:
+ * device int32, one for each token, or NULL (sz_kv_append_paged then rotates
+ * by the token's place in its sequence).  A position outside [0, table_len)
+ * is reported as SZ_ERR_INVALID_ARG on the device error word and the token
+ * left out. */
+typedef struct {
+    const float *table;
+    const int32_t *positions;
+    uint32_t table_len;
+    uint32_t rot;
+    uint32_t interleaved;
+    uint32_t reserved;
+} sz_rope_t;
+
+/* New tokens of every sequence, packed: rows cu_q[s] .. cu_q[s+1]-1 of the
+ * activations are sequence s's last tokens, and kv_len[s] is its length with
+ * them, so row cu_q[s] + i has place kv_len[s] - (cu_q[s+1] - cu_q[s]) + i.
+ * cu_q (device int32, seqs + 1, non-decreasing, from 0) and kv_len (device
+ * int32, seqs) are the same in sz_kv_append_paged and sz_attn_paged.  Rows
+ * from cu_q[seqs] on (a padded batch) are left as they are. */
+typedef struct {
+    uint64_t tokens; /* rows of the activations, below 2^31 */
+    sz_heads_t k;    /* kv_heads heads */
+    sz_heads_t v;    /* kv_heads heads */
+    sz_heads_t q;    /* optional: queries to normalise and rotate beside the keys */
+    sz_heads_t q_out;/* with q, and the same number of heads; may be q itself */
+    const int32_t *cu_q;
+    const int32_t *kv_len;
+    sz_head_norm_t norm;
+    sz_rope_t rope;
+} sz_kv_append_t;
+
+typedef struct {
+    uint64_t tokens;
+    sz_heads_t q; /* optional, with q_out; q_out may be q itself */
+    sz_heads_t q_out;
+    sz_heads_t k; /* optional, with k_out; k_out may be k itself */
+    sz_heads_t k_out;
+    sz_head_norm_t norm;
+    sz_rope_t rope; /* positions required where table is not NULL */
+    uint32_t head_dim;
+    uint32_t reserved;
+} sz_qk_norm_rope_t;
+
+typedef struct {
+    uint64_t tokens;
+    sz_heads_t q;   /* heads a multiple of kv_heads; query head h reads KV head h / (heads / kv_heads) */
+    sz_heads_t out; /* must not overlap q */
+    const int32_t *cu_q;
+    const int32_t *kv_len;
+    float *lse;     /* optional device float [tokens, heads]: natural log of the row's sum of exponentials */
+    float scale;    /* of the scores, positive and finite */
+    uint32_t causal;/* not 0: a row sees places up to its own; 0: every place below kv_len */
+    uint32_t window;/* w > 0: a row at place p sees no place below p - w + 1; 0: no window */
+    uint32_t reserved;
+} sz_attn_t;
+
+/* Workspace bytes of the operators: for a cache's sz_attn_paged and
+ * sz_kv_append_paged, or with NULL for sz_qk_norm_rope alone.  0 for an
+ * invalid cache. */
+size_t sz_ops_workspace_bytes(const sz_kv_cache_t *cache);
+
+/* Write k (normalised and rotated) and v into the cache at their tokens'
+ * places, and q, normalised and rotated, to q_out.  A token whose place is
+ * negative or beyond table_pages * page_tokens is reported as
+ * SZ_ERR_INVALID_ARG on the device error word and left out.  Two rows that
+ * name the same place of the same page race. */
+sz_status sz_kv_append_paged(const sz_kv_cache_t *cache, const sz_kv_append_t *args, void *d_ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/* Normalise and rotate query and key heads, out of place or in place. */
+sz_status sz_qk_norm_rope(const sz_qk_norm_rope_t *args, void *d_ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Attention of packed new tokens over the cache:
+ *     out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q . k_j)
+ * over the places j that the row sees (below kv_len, `causal`, `window`).  A
+ * row that sees none gives 0 and lse -infinity.  Places that a row does not
+ * see have no influence on it, whatever they hold.  The same inputs give the
+ * same bits.  A kv_len beyond the table is reported as SZ_ERR_INVALID_ARG on
+ * the device error word and the sequence cut there; so is a page outside the
+ * pool, whose places then count as holding zeros. */
+sz_status sz_attn_paged(const sz_kv_cache_t *cache, const sz_attn_t *args, void *d_ws, size_t ws_bytes,
+                        cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
