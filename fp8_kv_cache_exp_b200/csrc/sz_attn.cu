@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
     Work w;
     if (!work_begin<kSplitThreads, TR, kSplitBlock>(p, s_work, w)) return;
     for (;;) {
-        const Part t = work_part<TR, kSplitBlock>(p, w);
+        const Part t = work_part<TR, kSplitBlock>(p, w, blockIdx.x);
         const int32_t *ids = p.cache.table + uint64_t(w.seq) * p.cache.table_stride;
         // places of this CTA's part, whole steps of 16 (lo down to a step's start)
         const uint32_t part_lo = max((t.block0 + t.from) * kSplitBlock, t.r.lo / kPlaces * kPlaces);
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
         __syncthreads();
         if (written && t.s.q_len > 1) {
             for (uint32_t r = warp; r < t.rows; r += kSplitWarps)
-                if (s_bad[r]) attend_row<DT>(p, t.s, w.seq, w.head, t.r0 + r);
+                if (s_bad[r]) repair_row<DT>(p, t.s, w.seq, w.head, t.r0 + r, t.r);
             __syncthreads();
         }
         if (!work_next<TR>(p, w, t)) break;
@@ -478,6 +478,7 @@ template <int DT>
 sz_status run_dim(const AttnParams &p, int num_sms, cudaStream_t stream) {
     const uint32_t d = p.cache.head_dim;
     const uint64_t rows = cdiv(p.tokens, p.cache.seqs) * p.group.d;
+    if (d <= 128 && rows > 64) return launch_attn_tc(p, DT, num_sms, stream);
     if (d <= 64) return rows <= 16 ? run<DT, 64, 1>(p, num_sms, stream) : run<DT, 64, 2>(p, num_sms, stream);
     if (d <= 128) return rows <= 16 ? run<DT, 128, 1>(p, num_sms, stream) : run<DT, 128, 2>(p, num_sms, stream);
     return run<DT, 256, 1>(p, num_sms, stream);

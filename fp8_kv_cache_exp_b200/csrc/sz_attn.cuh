@@ -199,7 +199,7 @@ struct Part {
 };
 
 template <int TR, int BN>
-__device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w) {
+__device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w, uint32_t cta) {
     Part t;
     t.s = seq_info(p, w.seq);
     t.r = tile_range<TR>(p, t.s, w.tile);
@@ -210,7 +210,7 @@ __device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w) {
     t.from = w.from;
     t.to = uint32_t(min(uint64_t(t.n), w.from + (w.end - w.at)));
     if (t.from == 0 && t.to == t.n) {
-        t.c_first = t.c_last = blockIdx.x;
+        t.c_first = t.c_last = cta;
     } else {
         // block x belongs to the last CTA c with floor(total c / ctas) <= x
         const uint64_t x0 = w.at - w.from, x1 = x0 + t.n - 1;
@@ -291,6 +291,35 @@ __device__ __noinline__ void attend_row(const AttnParams &p, const SeqInfo &s, u
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (lane + 32 * j < d) out[lane + 32 * j] = uint16_t(pack_bf16(l == 0.f ? 0.f : o[j] / l, 0.f));
+}
+
+// A row whose result is not finite: right as it is unless a place that the row
+// does not see, but another row of its tile does (`tile` is what any of them
+// sees), holds a value that is not finite; then the row is done again by
+// itself.  All lanes of a warp call it.
+template <int DT>
+__device__ void repair_row(const AttnParams &p, const SeqInfo &s, uint32_t seq, uint32_t kvh, uint32_t row,
+                           const Range &tile) {
+    const uint32_t lane = threadIdx.x & 31, d = p.cache.head_dim;
+    const Range r = token_range(p, s, div_by(row, p.group));
+    const int32_t *ids = p.cache.table + uint64_t(seq) * p.cache.table_stride;
+    auto poisoned = [&](uint32_t lo, uint32_t hi) {
+        bool bad = false;
+        for (uint32_t t = lo; t < hi; ++t) {
+            const uint64_t off = place_offset(p.cache, p.ctl, ids, t);
+            if (off == kBadOffset) continue;
+            const uint8_t *v = p.cache.v + off + uint64_t(kvh) * d * (DT == SZ_BF16 ? 2 : 1);
+            for (uint32_t e = lane; e < d; e += 32) {
+                if constexpr (DT == SZ_BF16)
+                    bad = bad || (reinterpret_cast<const uint16_t *>(v)[e] & 0x7f80u) == 0x7f80u;
+                else
+                    bad = bad || (v[e] & 0x7cu) == 0x7cu;
+            }
+        }
+        return bool(__any_sync(0xffffffffu, bad));
+    };
+    if (poisoned(tile.lo, min(r.lo, tile.hi)) || poisoned(max(r.hi, tile.lo), tile.hi))
+        attend_row<DT>(p, s, seq, kvh, row);
 }
 
 }  // namespace sz

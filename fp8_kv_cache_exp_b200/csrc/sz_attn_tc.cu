@@ -1,0 +1,777 @@
+// sz_attn_tc.cu -- attention of many rows over a paged cache (sz_attn_paged) on
+// the fifth-generation tensor cores.
+//
+//   x = scale * q . k,  p = exp(x - m),  o = sum p v / sum p
+//
+// A CTA takes 256 rows of one sequence and KV head, as two tiles of 128, and
+// goes over their places in blocks of 128.  Scores, p and the sums of p v stay
+// in tensor memory: per tile 128 columns of scores, which p overwrites in 16
+// bits, and 128 columns of sums.  The roles:
+//   warps 0-3, 4-7  softmax of the first and the second tile, a thread a row:
+//                   a row's maximum and sum need no exchange between threads
+//   warps 8-11      keys, values and queries into shared memory
+//   warp 12         issues the products: per block p0 v, q0 k', p1 v, q1 k', so
+//                   that the tensor cores work on one tile while the other's
+//                   softmax runs
+// m is the largest score so far only to within 2^kSlack: the sums are rescaled
+// (through registers) when a row's maximum has grown by more, so that most
+// blocks leave them where they are.
+//
+// What bounds it: a block of 256 rows and heads of 128 is 2048 clocks of matrix
+// products and 2048 clocks of ex2 (16 a clock).
+//
+// The cache's pages are of any size and lie anywhere, so rows are fetched one by
+// one, by 16-byte asynchronous copies into the swizzled layout that the products
+// read.  An E5M2 cache's rows are copied as they are and spread to fp16 (E5M2 is
+// fp16's upper byte) on their way to that layout; queries are then fp16 too,
+// behind a power of two for each row that brings the row's largest below 2^14.
+//
+// A second kernel, which starts as the first one ends, joins the tiles that
+// several CTAs share, spread over all SMs.
+#include "sz_attn.cuh"
+
+namespace sz {
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+
+constexpr int kTcThreads = 512;
+constexpr int kTcRows = 256;
+constexpr int kTcBlock = 128;
+constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows of 64 16-bit elements
+// registers of a softmax thread and of the others: 256 * 200 + 256 * 56 = 512 * 128,
+// what the CTA is launched with
+#define SZ_TC_REGS_SOFTMAX "200"
+#define SZ_TC_REGS_OTHER "56"
+
+template <int DT, int DP>
+struct TcCfg {
+    static constexpr uint32_t EB = DT == SZ_BF16 ? 2 : 1;
+    static constexpr uint32_t PANELS = DP / 64;
+    static constexpr uint32_t STAGE = PANELS * kPanel;       // 128 rows
+    static constexpr uint32_t STAGES = DP == 64 ? 6 : (DT == SZ_BF16 ? 5 : 4);
+    static constexpr uint32_t RAW = 128 * DP;                // E5M2: 128 rows as they come
+    static constexpr uint32_t RAWS = DT == SZ_BF16 ? 0 : (DP == 64 ? 4 : 2);
+    static constexpr uint32_t RING_AT = 2 * STAGE;           // behind the queries
+    static constexpr uint32_t RAW_AT = RING_AT + STAGES * STAGE;
+    static constexpr uint32_t AUX_AT = RAW_AT + RAWS * RAW;
+    static constexpr uint32_t SMEM = AUX_AT + 1024 + 1024;   // barriers and exponents; slack to align the base
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(sizeof(WorkScratch<kTcThreads>) <= STAGES * STAGE, "the scratch lies in the ring");
+    // p's factor 2^RAISE keeps small weights among fp16's normal numbers; 2^(RAISE + SLACK) is in its range
+    static constexpr float RAISE = DT == SZ_BF16 ? 0.f : 8.f;
+    static constexpr float SLACK = DT == SZ_BF16 ? 8.f : 6.f;
+};
+
+struct TcAux {
+    uint64_t full[8], empty[8];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t drain;
+    uint32_t tmem, abort, bad;
+    int8_t exp[kTcRows];  // E5M2: exponent taken out of each query row
+};
+static_assert(sizeof(TcAux) <= 1024, "aux");
+
+// What a CTA leaves for the joining kernel: its share, and the tile of it that
+// it shares with later CTAs only.
+struct TcDesc {
+    Work begin, join;
+    uint32_t bad;    // rows of its own tiles came out not finite
+    uint32_t joins;  // `join` is one
+    uint32_t has, pad;
+};
+static_assert(sizeof(TcDesc) * kMaxSms <= kDescBytes, "descriptors");
+
+// Waits are bounded: after the limit the CTA gives up (every role then leaves
+// its loop) and the error word says so.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, TcAux *aux, uint32_t *ctl) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63) == 0) {
+            if (*reinterpret_cast<volatile uint32_t *>(&aux->abort)) return false;
+            if (global_ns() - t0 > kWaitLimitNs) {
+                *reinterpret_cast<volatile uint32_t *>(&aux->abort) = 1;
+                set_error(ctl, SZ_ERR_TIMEOUT, blockIdx.x);
+                return false;
+            }
+        }
+    }
+}
+// All lanes wait, and go on together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, TcAux *aux, uint32_t *ctl) {
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, aux, ctl));
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void sts_u128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// ------------------------------------------------------------ tensor memory
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+#define SZ_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+#define SZ_R16(r, i) SZ_R4(r, i), SZ_R4(r, i + 4), SZ_R4(r, i + 8), SZ_R4(r, i + 12)
+#define SZ_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+#define SZ_I16(r, i) SZ_I4(r, i), SZ_I4(r, i + 4), SZ_I4(r, i + 8), SZ_I4(r, i + 12)
+
+// 16 or 32 neighbouring columns of the thread's row.
+__device__ __forceinline__ void tc_ld16(uint32_t *r, uint32_t a) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : SZ_R16(r, 0) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t *r, uint32_t a) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : SZ_R16(r, 0), SZ_R16(r, 16) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
+            SZ_I16(r, 0), "r"(a) : "memory");
+}
+
+// Shared-memory descriptor of rows of 128 bytes, 8 rows to a swizzle atom:
+// leading offset (from one 64-element panel to the next, where the matrix runs
+// along the row), stride offset of 1024 bytes from 8 rows to the next.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t a) {
+    return uint64_t((a >> 4) & 0x3fff) | uint64_t(kPanel >> 4) << 16 | uint64_t(1024 >> 4) << 32 | 1ull << 46 |
+           2ull << 61;
+}
+
+// d += a b: both operands 16-bit (fp16, or bf16), sums in 32 bits, 128 rows.
+__device__ __forceinline__ uint32_t instr_desc(int dt, uint32_t n, bool b_along_n) {
+    const uint32_t t = dt == SZ_BF16 ? 1 : 0;
+    return 1u << 4 | t << 7 | t << 10 | (b_along_n ? 1u << 16 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
+}
+
+// Two floats at a time.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// ------------------------------------------------------------------- roles
+
+// Keys, values and queries into shared memory (warps 8-11).
+template <int DT, int DP>
+__device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux) {
+    using C = TcCfg<DT, DP>;
+    constexpr uint32_t LPR = DP * C::EB / 16;  // lanes to a row of the cache
+    constexpr uint32_t ROWS = 32 / LPR;
+    const uint32_t tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
+    const uint32_t d = p.cache.head_dim, G = p.group.d;
+    const uint32_t piece = lane % LPR, row0 = warp * 32 + lane / LPR;
+    const bool has_piece = piece * 16 < d * C::EB;
+    // tiles of keys and values, in the order in which they are used; what is behind `ready` has been handed over
+    uint32_t issued = 0, ready = 0;
+    auto hand_over = [&](uint32_t to) {
+        if (ready == to) return;
+        fence_proxy_async_smem();
+        for (; ready < to; ++ready) bar_arrive(&aux->full[ready % C::STAGES]);
+    };
+    auto stage_free = [&](uint32_t n) {
+        if (n < C::STAGES) return true;
+        return bool(__all_sync(0xffffffffu, mbar_try_wait(&aux->empty[n % C::STAGES], (n / C::STAGES - 1) & 1)));
+    };
+    auto wait_free = [&](uint32_t n) {
+        return n < C::STAGES || warp_wait(&aux->empty[n % C::STAGES], (n / C::STAGES - 1) & 1, aux, p.ctl);
+    };
+    for (uint32_t parts = 0;; ++parts) {
+        const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
+        const int32_t *ids = p.cache.table + uint64_t(w.seq) * p.cache.table_stride;
+        const uint32_t part_hi = min((t.block0 + t.to) * kTcBlock, t.r.hi);
+        const uint64_t head_off = uint64_t(w.head) * d * C::EB + piece * 16;
+
+        // queries, once the last part's products with them are done
+        if (parts > 0) {
+            if (!warp_wait(&aux->q_empty, (parts - 1) & 1, aux, p.ctl)) return;
+        }
+        const uint32_t q_rows = t.rows > 128 ? 256 : 128;
+        if constexpr (DT == SZ_BF16) {
+            constexpr uint32_t QL = DP / 8;
+            const uint32_t c = tid % QL;
+            for (uint32_t r = tid / QL; r < q_rows; r += 128 / QL) {
+                const bool in = r < t.rows;
+                const uint32_t g = t.r0 + (in ? r : 0), i = div_by(g, p.group);
+                const uint8_t *src = p.q.p + uint64_t(t.s.q0 + i) * p.q.ts + uint64_t(w.head * G + (g - i * G)) * p.q.hs;
+                const uint32_t dst = base + (r / 128) * C::STAGE + (c / 8) * kPanel + (r % 128) * 128 +
+                                     (((c % 8) ^ (r & 7)) << 4);
+                if (c * 8 < d) cp_async16(dst, src + c * 16, in);
+            }
+            cp_commit();
+            cp_wait<0>();
+            hand_over(issued);
+        } else {
+            constexpr uint32_t QL = DP / 8;
+            const uint32_t c = tid % QL;
+#pragma unroll 4
+            for (uint32_t r = tid / QL; r < q_rows; r += 128 / QL) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < t.rows && c * 8 < d) {
+                    const uint32_t i = div_by(t.r0 + r, p.group);
+                    v = *reinterpret_cast<const uint4 *>(p.q.p + uint64_t(t.s.q0 + i) * p.q.ts +
+                                                         uint64_t(w.head * G + (t.r0 + r - i * G)) * p.q.hs + c * 16);
+                }
+                uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                float top = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
+#pragma unroll
+                for (int o = QL / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                int e = 0;
+                if (top > 0.f && top < INFINITY) e = min(13 - (int(__float_as_uint(top) >> 23) - 127), 120);
+                const float up = __uint_as_float(uint32_t(127 + e) << 23);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = pack_f16(bf16_lo(x[j]) * up, bf16_hi(x[j]) * up);
+                if (c * 8 < d)
+                    sts_u128(base + (r / 128) * C::STAGE + (c / 8) * kPanel + (r % 128) * 128 + (((c % 8) ^ (r & 7)) << 4),
+                             make_uint4(x[0], x[1], x[2], x[3]));
+                if (c == 0) aux->exp[r] = int8_t(e);
+            }
+        }
+        fence_proxy_async_smem();
+        bar_arrive(&aux->q_full);
+
+        // the place of this lane's row of a block, and its page's id
+        auto place = [&](uint32_t j) { return (t.block0 + j) * kTcBlock + warp * 32 + lane; };
+        auto page_id = [&](uint32_t j) -> int32_t {
+            const uint32_t at = place(j);
+            return j < t.to && at >= t.r.lo && at < part_hi ? __ldg(ids + div_by(at, p.cache.page_tokens)) : 0;
+        };
+        auto offset = [&](uint32_t j, int32_t id) -> uint64_t {
+            const uint32_t at = place(j);
+            if (at < t.r.lo || at >= part_hi) return kBadOffset;
+            const uint32_t page = div_by(at, p.cache.page_tokens);
+            if (id < 0 || uint64_t(id) >= p.cache.pool_pages) {
+                set_error(p.ctl, SZ_ERR_INVALID_ARG, page);
+                return kBadOffset;
+            }
+            return uint64_t(id) * p.cache.page_bytes + uint64_t(at - page * p.cache.page_tokens.d) * p.cache.row_bytes;
+        };
+        int32_t id = page_id(t.from);
+        uint64_t off = 0;
+        if constexpr (DT == SZ_BF16) {
+            for (uint32_t n = 0; n < 2 * (t.to - t.from); ++n) {
+                const uint32_t j = t.from + n / 2;
+                if ((n & 1) == 0) {
+                    off = offset(j, id);
+                    id = page_id(j + 1);
+                }
+                if (!stage_free(issued)) {
+                    cp_wait<0>();
+                    hand_over(issued);
+                    if (!wait_free(issued)) return;
+                }
+                const uint8_t *pool = (n & 1) ? p.cache.v : p.cache.k;
+                const uint32_t dst = base + C::RING_AT + (issued % C::STAGES) * C::STAGE + (piece / 8) * kPanel;
+#pragma unroll 8
+                for (uint32_t r = 0; r < 32; r += ROWS) {
+                    const uint64_t o = __shfl_sync(0xffffffffu, off, int(r + lane / LPR));
+                    const uint32_t row = row0 + r;
+                    const bool in = o != kBadOffset;
+                    if (has_piece)
+                        cp_async16(dst + row * 128 + (((piece % 8) ^ (row & 7)) << 4), pool + (in ? o + head_off : 0), in);
+                }
+                cp_commit();
+                ++issued;
+                cp_wait<2>();
+                if (issued > 2) hand_over(max(ready, issued - 2));
+            }
+            cp_wait<0>();
+            hand_over(issued);
+        } else {
+            const uint32_t tiles = 2 * (t.to - t.from);
+            const uint32_t raw = base + C::RAW_AT + tid * 16;
+            for (uint32_t n = 0; n < tiles + C::RAWS - 1; ++n) {
+                if (n < tiles) {
+                    const uint32_t j = t.from + n / 2;
+                    if ((n & 1) == 0) {
+                        off = offset(j, id);
+                        id = page_id(j + 1);
+                    }
+                    const uint8_t *pool = (n & 1) ? p.cache.v : p.cache.k;
+#pragma unroll
+                    for (uint32_t r = 0; r < 32; r += ROWS) {
+                        const uint64_t o = __shfl_sync(0xffffffffu, off, int(r + lane / LPR));
+                        const bool in = o != kBadOffset;
+                        if (has_piece)
+                            cp_async16(raw + (n % C::RAWS) * C::RAW + (r / ROWS) * 2048, pool + (in ? o + head_off : 0), in);
+                    }
+                }
+                cp_commit();
+                if (n + 1 < C::RAWS) continue;
+                const uint32_t m = n + 1 - C::RAWS;  // the tile that has come
+                cp_wait<C::RAWS - 1>();
+                if (!wait_free(issued)) return;
+                const uint32_t dst = base + C::RING_AT + (issued % C::STAGES) * C::STAGE + (piece / 4) * kPanel;
+                if (has_piece) {
+#pragma unroll
+                    for (uint32_t r = 0; r < 32; r += ROWS) {
+                        const uint4 v = lds_u128(raw + (m % C::RAWS) * C::RAW + (r / ROWS) * 2048);
+                        const uint4 lo = make_uint4(prmt(v.x, 0, 0x1404), prmt(v.x, 0, 0x3424), prmt(v.y, 0, 0x1404),
+                                                    prmt(v.y, 0, 0x3424));
+                        const uint4 hi = make_uint4(prmt(v.z, 0, 0x1404), prmt(v.z, 0, 0x3424), prmt(v.w, 0, 0x1404),
+                                                    prmt(v.w, 0, 0x3424));
+                        const uint32_t row = row0 + r, a = dst + row * 128, ch = 2 * (piece % 4);
+                        // the lanes of the second panel go the other way round, off the first one's banks
+                        const bool odd = piece >= 4;
+                        sts_u128(a + (((ch + (odd ? 1 : 0)) ^ (row & 7)) << 4), odd ? hi : lo);
+                        sts_u128(a + (((ch + (odd ? 0 : 1)) ^ (row & 7)) << 4), odd ? lo : hi);
+                    }
+                }
+                ++issued;
+                hand_over(issued);
+            }
+        }
+        if (!work_next<kTcRows>(p, w, t)) return;
+    }
+}
+
+// The products (one thread).
+template <int DT, int DP>
+__device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux, uint32_t tmem) {
+    using C = TcCfg<DT, DP>;
+    const uint32_t d = p.cache.head_dim, ksteps = d / 16;
+    const uint32_t qk_desc = instr_desc(DT, kTcBlock, false), pv_desc = instr_desc(DT, d, true);
+    uint32_t kv = 0, p_uses[2] = {0, 0};
+    auto full = [&](uint32_t n) {
+        const bool ok = bar_wait(&aux->full[n % C::STAGES], (n / C::STAGES) & 1, aux, p.ctl);
+        tc_after();
+        return ok;
+    };
+    auto stage = [&](uint32_t n) { return smem_desc(base + C::RING_AT + (n % C::STAGES) * C::STAGE); };
+    auto release = [&](uint32_t n) { tc_commit(&aux->empty[n % C::STAGES]); };
+    auto qk = [&](uint32_t i, uint32_t n) {
+        const uint64_t a = smem_desc(base + i * C::STAGE), b = stage(n);
+        for (uint32_t k = 0; k < ksteps; ++k) {
+            const uint64_t o = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
+            mma_ss(tmem + i * 128, a + o, b + o, qk_desc, k > 0);
+        }
+        tc_commit(&aux->s_full[i]);
+    };
+    auto pv = [&](uint32_t i, uint32_t n, bool add) {
+        if (!bar_wait(&aux->p_full[i], p_uses[i]++ & 1, aux, p.ctl)) return false;
+        tc_after();
+        const uint64_t b = stage(n);
+#pragma unroll
+        for (uint32_t k = 0; k < kTcBlock / 16; ++k)
+            mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b + k * (2048 >> 4), pv_desc, add || k > 0);
+        return true;
+    };
+    for (uint32_t parts = 0;; ++parts) {
+        const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
+        const uint32_t n = t.to - t.from;
+        const bool two = t.rows > 128;
+        if (!bar_wait(&aux->q_full, parts & 1, aux, p.ctl)) return;
+        tc_after();
+        if (!full(kv)) return;
+        qk(0, kv);
+        if (two) qk(1, kv);
+        release(kv);
+        if (n == 1) tc_commit(&aux->q_empty);
+        for (uint32_t j = 0; j < n; ++j) {
+            const uint32_t v = kv + 1, k = kv + 2;
+            const bool more = j + 1 < n;
+            if (!full(v)) return;
+            if (!pv(0, v, j > 0)) return;
+            if (more) {
+                if (!full(k)) return;
+                qk(0, k);
+            } else {
+                tc_commit(&aux->o_full[0]);
+            }
+            if (two) {
+                if (!pv(1, v, j > 0)) return;
+                release(v);
+                if (more) qk(1, k);
+                else tc_commit(&aux->o_full[1]);
+            } else {
+                release(v);
+            }
+            if (more) {
+                release(k);
+                if (j + 2 == n) tc_commit(&aux->q_empty);
+            }
+            kv += 2;
+        }
+        if (!work_next<kTcRows>(p, w, t)) return;
+    }
+}
+
+// Softmax of one tile's rows, a thread a row, and what becomes of the sums.
+template <int DT, int DP>
+__device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux *aux, uint32_t tmem, TcDesc *desc) {
+    using C = TcCfg<DT, DP>;
+    const uint32_t i = threadIdx.x / 128, row = threadIdx.x & 127;
+    const uint32_t lanes = (threadIdx.x & 96) << 16;  // the warp's quarter of tensor memory
+    const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * 128;
+    const uint32_t d = p.cache.head_dim, G = p.group.d;
+    uint32_t s_uses = 0, o_uses = 0;
+    for (uint32_t parts = 0;; ++parts) {
+        const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
+        const bool whole_tile = t.c_first == t.c_last;
+        if (threadIdx.x == 0 && !whole_tile && t.c_first == blockIdx.x) {
+            desc->join = w;
+            desc->joins = 1;
+        }
+        // every warp sees every part's queries come, whether it has rows or not: their next ones wait for it
+        const uint32_t r = i * 128 + row;
+        if (!warp_wait(&aux->q_full, parts & 1, aux, p.ctl)) return;
+        float sc = p.scale_log2;
+        if constexpr (DT == SZ_FP8_E5M2) sc *= __uint_as_float(uint32_t(127 - aux->exp[r]) << 23);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bar_arrive(&aux->q_empty);
+        if (i == 0 || t.rows > 128) {
+            Range rr{0, 0};
+            if (r < t.rows) rr = token_range(p, t.s, div_by(t.r0 + r, p.group));
+            // every row of the 128 sees [full_lo, full_hi)
+            const uint32_t full_hi = token_range(p, t.s, div_by(t.r0 + i * 128, p.group)).hi;
+            const uint32_t full_lo = token_range(p, t.s, div_by(t.r0 + min(i * 128 + 128, t.rows) - 1, p.group)).lo;
+            float m = -INFINITY, l = 0.f;
+            for (uint32_t j = t.from; j < t.to; ++j) {
+                if (!warp_wait(&aux->s_full[i], s_uses++ & 1, aux, p.ctl)) return;
+                tc_after();
+                uint32_t x[128];
+                tc_ld32(x, s_at);
+                tc_ld32(x + 32, s_at + 32);
+                tc_ld32(x + 64, s_at + 64);
+                tc_ld32(x + 96, s_at + 96);
+                tc_wait_ld();
+                const uint32_t at = (t.block0 + j) * kTcBlock;
+                if (at < full_lo || at + kTcBlock > full_hi) {
+                    // columns [a, b) of the block are seen
+                    const uint32_t a = rr.lo > at ? rr.lo - at : 0, b = rr.hi > at ? rr.hi - at : 0;
+#pragma unroll
+                    for (uint32_t c = 0; c < 128; ++c)
+                        if (c < a || c >= b) x[c] = 0xff800000u;
+                }
+                float tops[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tops[c] = __uint_as_float(x[c]);
+#pragma unroll
+                for (int c = 4; c < 128; ++c) tops[c & 3] = fmaxf(tops[c & 3], __uint_as_float(x[c]));
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * sc;
+                const bool grows = top > m + C::SLACK;
+                if (__any_sync(0xffffffffu, grows)) {
+                    const float c = grows ? exp2_fast(m - top) : 1.f;
+                    if (grows) m = top;
+                    l *= c;
+                    if (j > t.from) {
+                        for (uint32_t k = 0; k < d; k += 16) {
+                            uint32_t o[16];
+                            tc_ld16(o, o_at + k);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
+                            tc_st16(o_at + k, o);
+                        }
+                    }
+                }
+                const float shift = C::RAISE - (m == -INFINITY ? 0.f : m);
+                const uint64_t sc2 = f2(sc, sc), shift2 = f2(shift, shift);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, b;
+                        f2_split(f2_fma(f2(__uint_as_float(x[c + e]), __uint_as_float(x[c + e + 1])), sc2, shift2), a, b);
+                        a = exp2_fast(a);
+                        b = exp2_fast(b);
+                        sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2(a, b));
+                        pk[e / 2] = DT == SZ_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
+                    }
+                    tc_st16(s_at + c / 2, pk);
+                }
+                tc_wait_st();
+                tc_before();
+                bar_arrive(&aux->p_full[i]);
+                float a, b;
+                f2_split(f2_add(sum[0], sum[1]), a, b);
+                l += a + b;
+            }
+            if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p.ctl)) return;
+            tc_after();
+            if (whole_tile) {
+                const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
+                const float f = l == 0.f ? 0.f : 1.f / l;
+                uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs;
+                float worst = 0.f;
+                for (uint32_t k = 0; k < d; k += 16) {
+                    uint32_t o[16];
+                    tc_ld16(o, o_at + k);
+                    tc_wait_ld();
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float a = __uint_as_float(o[2 * e]) * f, b = __uint_as_float(o[2 * e + 1]) * f;
+                        worst = fmaf(0.f, a, fmaf(0.f, b, worst));  // stays 0, or is NaN
+                        pk[e] = pack_bf16(a, b);
+                    }
+                    if (r < t.rows) {
+                        *reinterpret_cast<uint4 *>(out + 2 * k) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        *reinterpret_cast<uint4 *>(out + 2 * k + 16) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    }
+                }
+                if (r < t.rows) {
+                    if (p.lse)
+                        p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] =
+                            l == 0.f ? -INFINITY : kLn2 * (m - C::RAISE + log2f(l));
+                    if (worst != 0.f) aux->bad = 1;
+                }
+            } else {
+                // columns of 256 rows, then the rows' m and l
+                float *part = p.part + uint64_t(part_slot(blockIdx.x, t)) * kTcRows * (d + 2) + r;
+                for (uint32_t k = 0; k < d; k += 16) {
+                    uint32_t o[16];
+                    tc_ld16(o, o_at + k);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) part[(k + e) * kTcRows] = __uint_as_float(o[e]);
+                }
+                part[d * kTcRows] = m;
+                part[(d + 1) * kTcRows] = l;
+            }
+            // the sums are read before the next part's first weights are announced
+            tc_before();
+        }
+        if (!work_next<kTcRows>(p, w, t)) return;
+    }
+}
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
+    using C = TcCfg<DT, DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t base = smem_u32(smem);
+    TcAux *aux = reinterpret_cast<TcAux *>(smem + C::AUX_AT);
+    const uint32_t tid = threadIdx.x, warp = tid >> 5;
+    TcDesc *desc = reinterpret_cast<TcDesc *>(p.desc) + blockIdx.x;
+
+    if (tid == 0) {
+        for (uint32_t i = 0; i < C::STAGES; ++i) {
+            mbar_init(&aux->full[i], 128);
+            mbar_init(&aux->empty[i], 1);
+        }
+        mbar_init(&aux->q_full, 128);
+        mbar_init(&aux->q_empty, 1 + 8);  // the products, and the softmax's warps
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&aux->s_full[i], 1);
+            mbar_init(&aux->p_full[i], 128);
+            mbar_init(&aux->o_full[i], 1);
+        }
+        mbar_init(&aux->drain, 1);
+        fence_mbar_init();
+        aux->abort = 0;
+        aux->bad = 0;
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    Work w;
+    const bool has = work_begin<kTcThreads, kTcRows, kTcBlock>(
+        p, *reinterpret_cast<WorkScratch<kTcThreads> *>(smem + C::RING_AT), w);
+    if (tid == 0) {
+        desc->joins = 0;
+        desc->has = has;
+        desc->bad = 0;
+        if (has) desc->begin = w;
+    }
+    if (!has) return;
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&aux->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // the scratch's last reads are done before the copies write over it
+    fence_proxy_async_smem();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&aux->tmem);
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 " SZ_TC_REGS_SOFTMAX ";");
+        softmax_role<DT, DP>(p, w, aux, tmem, desc);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 " SZ_TC_REGS_OTHER ";");
+        if (warp < 12) {
+            load_role<DT, DP>(p, w, base, aux);
+            cp_wait<0>();
+        } else if (tid == 12 * 32) {
+            mma_role<DT, DP>(p, w, base, aux, tmem);
+            // nothing of this CTA's is under way when it gives its memory back
+            tc_commit(&aux->drain);
+            bar_wait(&aux->drain, 0, aux, p.ctl);
+        }
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (tid == 0 && aux->bad) desc->bad = 1;
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ------------------------------------------------------------------ joining
+
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 32;
+constexpr int kJoinSlices = kTcRows / kJoinRows;
+
+// CTA (c, slice): 32 rows of the tile that CTA c began and others ended, a lane
+// a row, a quarter of the columns to a warp.
+template <int DT, int DP>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p) {
+    using C = TcCfg<DT, DP>;
+    __shared__ float s_f[kMaxSms][kJoinRows];
+    __shared__ uint32_t s_bad;
+    pdl_wait();
+    pdl_launch_dependents();
+    const uint32_t c = blockIdx.x / kJoinSlices, slice = blockIdx.x % kJoinSlices;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t d = p.cache.head_dim, G = p.group.d;
+    const TcDesc *desc = reinterpret_cast<const TcDesc *>(p.desc) + c;
+    if (!desc->has) return;
+    if (desc->joins) {
+        const Work w = desc->join;
+        const Part t = work_part<kTcRows, kTcBlock>(p, w, c);
+        if (slice * kJoinRows < t.rows) {
+            const uint32_t r = slice * kJoinRows + lane, parts = t.c_last - t.c_first + 1;
+            if (threadIdx.x == 0) s_bad = 0;
+            auto slot = [&](uint32_t k) {
+                return p.part + uint64_t(part_slot(t.c_first + k, t)) * kTcRows * (d + 2) + r;
+            };
+            float M = -INFINITY, L = 0.f;
+            for (uint32_t k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(slot(k) + d * kTcRows));
+            const float safe = M == -INFINITY ? 0.f : M;
+            for (uint32_t k = 0; k < parts; ++k) {
+                const float f = exp2_fast(__ldcg(slot(k) + d * kTcRows) - safe);
+                if (warp == 0) s_f[k][lane] = f;
+                L += f * __ldcg(slot(k) + (d + 1) * kTcRows);
+            }
+            __syncthreads();
+            const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs;
+            float worst = 0.f;
+            for (uint32_t e = warp * (d / 4); e < (warp + 1) * (d / 4); e += 4) {
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (uint32_t k = 0; k < parts; ++k) {
+                    const float f = s_f[k][lane];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = fmaf(f, __ldcg(slot(k) + (e + j) * kTcRows), v[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] *= inv;
+                    worst = fmaf(0.f, v[j], worst);
+                }
+                if (r < t.rows)
+                    *reinterpret_cast<uint2 *>(out + 2 * e) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            }
+            if (warp == 0 && r < t.rows && p.lse)
+                p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] = L == 0.f ? -INFINITY : kLn2 * (M - C::RAISE + log2f(L));
+            if (r < t.rows && worst != 0.f) atomicOr(&s_bad, 1u << lane);
+            __syncthreads();
+            for (uint32_t bad = s_bad, k = 0; bad; bad &= bad - 1, ++k) {
+                const uint32_t x = __ffs(bad) - 1;
+                if (k % (kJoinThreads / 32) == warp)
+                    repair_row<DT>(p, t.s, w.seq, w.head, t.r0 + slice * kJoinRows + x, t.r);
+            }
+        }
+    }
+    if (desc->bad) {
+        // rows of the CTA's own tiles that are not finite
+        Work w = desc->begin;
+        for (;;) {
+            const Part t = work_part<kTcRows, kTcBlock>(p, w, c);
+            if (t.c_first == t.c_last)
+                for (uint32_t r = slice * (kJoinThreads / 32) + warp; r < t.rows; r += kJoinSlices * (kJoinThreads / 32)) {
+                    const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
+                    const uint16_t *out = reinterpret_cast<const uint16_t *>(
+                        p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs);
+                    bool bad = false;
+                    for (uint32_t e = lane; e < d; e += 32) bad = bad || (out[e] & 0x7f80u) == 0x7f80u;
+                    if (__any_sync(0xffffffffu, bad)) repair_row<DT>(p, t.s, w.seq, w.head, g, t.r);
+                }
+            if (!work_next<kTcRows>(p, w, t)) break;
+        }
+    }
+}
+
+template <int DT, int DP>
+sz_status run(const AttnParams &p, int num_sms, cudaStream_t stream) {
+    using C = TcCfg<DT, DP>;
+    static std::atomic<int> cache[kMaxDevices];
+    auto kern = attn_tc_kernel<DT, DP>;
+    if (resident_per_sm(reinterpret_cast<const void *>(kern), kTcThreads, C::SMEM, cache) <= 0) return SZ_ERR_CUDA;
+    if (launch_pdl(kern, unsigned(num_sms), kTcThreads, C::SMEM, stream, p) != cudaSuccess) return SZ_ERR_CUDA;
+    return launch_pdl(attn_join_kernel<DT, DP>, unsigned(num_sms) * kJoinSlices, kJoinThreads, 0, stream, p) ==
+                   cudaSuccess
+               ? SZ_OK
+               : SZ_ERR_CUDA;
+}
+
+}  // namespace
+
+sz_status launch_attn_tc(const AttnParams &p, int dtype, int num_sms, cudaStream_t stream) {
+    if (dtype == SZ_BF16)
+        return p.cache.head_dim <= 64 ? run<SZ_BF16, 64>(p, num_sms, stream) : run<SZ_BF16, 128>(p, num_sms, stream);
+    return p.cache.head_dim <= 64 ? run<SZ_FP8_E5M2, 64>(p, num_sms, stream)
+                                  : run<SZ_FP8_E5M2, 128>(p, num_sms, stream);
+}
+
+}  // namespace sz

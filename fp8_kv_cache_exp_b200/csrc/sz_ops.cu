@@ -138,7 +138,7 @@ extern "C" {
 size_t sz_ops_workspace_bytes(const sz_kv_cache_t *cache) {
     if (!cache) return size_t(kCtlWords) * 4;
     if (check_cache(cache) != SZ_OK) return 0;
-    return size_t(kCtlWords) * 4 + kArrivedBytes + attn_part_floats(cache->head_dim) * 4 + 16;
+    return size_t(kCtlWords) * 4 + kArrivedBytes + kDescBytes + attn_part_floats(cache->head_dim) * 4 + 16;
 }
 
 sz_status sz_kv_append_paged(const sz_kv_cache_t *cache, const sz_kv_append_t *a, void *d_ws, size_t ws_bytes,
@@ -239,9 +239,9 @@ sz_status sz_attn_paged(const sz_kv_cache_t *cache, const sz_attn_t *a, void *d_
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
     p.ctl = reinterpret_cast<uint32_t *>(ws);
     p.arrived = reinterpret_cast<uint32_t *>(ws + size_t(kCtlWords) * 4);
+    p.desc = ws + size_t(kCtlWords) * 4 + kArrivedBytes;
     // the workspace is 8-byte aligned, partials are read and written 16 bytes at a time
-    p.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws + size_t(kCtlWords) * 4 + kArrivedBytes) + 15) &
-                                       ~uintptr_t(15));
+    p.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(p.desc + kDescBytes) + 15) & ~uintptr_t(15));
     p.cache = cache_ref(*cache);
     p.q = heads_ref(a->q);
     p.out = heads_ref(a->out);

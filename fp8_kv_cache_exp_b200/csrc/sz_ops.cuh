@@ -63,6 +63,7 @@ struct RopeParams {
 struct AttnParams {
     uint32_t *ctl;
     uint32_t *arrived;   // one counter for each CTA, zero between calls
+    uint8_t *desc;       // what a CTA of the tensor-memory kernel leaves for the joining one
     float *part;         // partial results, two slots for each CTA
     CacheRef cache;
     HeadsRef q, out;
@@ -132,13 +133,15 @@ __device__ __forceinline__ uint32_t pack_e5m2(float lo, float hi) {
 // Launchers (sz_rope.cu, sz_attn.cu, sz_attn_tc.cu).
 sz_status launch_rope(const RopeParams &p, bool append, int dtype, int num_sms, cudaStream_t stream);
 sz_status launch_attn(const AttnParams &p, int dtype, int num_sms, cudaStream_t stream);
+sz_status launch_attn_tc(const AttnParams &p, int dtype, int num_sms, cudaStream_t stream);
 
 // Workspace of sz_attn_paged behind the 256-byte control block: arrival
-// counters, then partial results.  A partial is kPartRows rows of a head's
+// counters, descriptors, then partial results.  A partial is kPartRows rows of a head's
 // sums in float and two statistics a row.
 constexpr uint32_t kMaxSms = 160;
 constexpr uint32_t kAttnCtas = 3 * kMaxSms;  // most CTAs of any attention kernel
 constexpr size_t kArrivedBytes = size_t(kAttnCtas) * 4;
+constexpr size_t kDescBytes = size_t(kMaxSms) * 128;
 // floats of all partials: the largest (CTAs * rows) of the kernels is a
 // persistent CTA for each SM with 256 rows, or kAttnCtas of 32
 constexpr size_t attn_part_floats(uint32_t head_dim) { return size_t(2) * kMaxSms * 256 * (head_dim + 2); }
