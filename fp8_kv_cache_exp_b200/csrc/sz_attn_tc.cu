@@ -131,6 +131,12 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
                  : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
 #define SZ_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
 #define SZ_R16(r, i) SZ_R4(r, i), SZ_R4(r, i + 4), SZ_R4(r, i + 8), SZ_R4(r, i + 12)
 #define SZ_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
@@ -377,48 +383,62 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
     }
 }
 
-// The products (one thread).
+// The products.  The warp goes through the loop together and one elected lane
+// issues: behind a test of the thread's own number the compiler does not see
+// that one lane is left, and each product took twice as long.
 template <int DT, int DP>
 __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux, uint32_t tmem) {
     using C = TcCfg<DT, DP>;
     const uint32_t d = p.cache.head_dim, ksteps = d / 16;
     const uint32_t qk_desc = instr_desc(DT, kTcBlock, false), pv_desc = instr_desc(DT, d, true);
+    const bool leader = elect_one();
     uint32_t kv = 0, p_uses[2] = {0, 0};
     auto full = [&](uint32_t n) {
-        const bool ok = bar_wait(&aux->full[n % C::STAGES], (n / C::STAGES) & 1, aux, p.ctl);
+        const bool ok = warp_wait(&aux->full[n % C::STAGES], (n / C::STAGES) & 1, aux, p.ctl);
         tc_after();
         return ok;
     };
     auto stage = [&](uint32_t n) { return smem_desc(base + C::RING_AT + (n % C::STAGES) * C::STAGE); };
-    auto release = [&](uint32_t n) { tc_commit(&aux->empty[n % C::STAGES]); };
+    auto commit = [&](uint64_t *bar) {
+        if (leader) tc_commit(bar);
+        __syncwarp();
+    };
+    auto release = [&](uint32_t n) { commit(&aux->empty[n % C::STAGES]); };
     auto qk = [&](uint32_t i, uint32_t n) {
         const uint64_t a = smem_desc(base + i * C::STAGE), b = stage(n);
-        for (uint32_t k = 0; k < ksteps; ++k) {
-            const uint64_t o = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
-            mma_ss(tmem + i * 128, a + o, b + o, qk_desc, k > 0);
+        if (leader) {
+#pragma unroll
+            for (uint32_t k = 0; k < DP / 16; ++k) {
+                const uint64_t o = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
+                if (k < ksteps) mma_ss(tmem + i * 128, a + o, b + o, qk_desc, k > 0);
+            }
+            tc_commit(&aux->s_full[i]);
         }
-        tc_commit(&aux->s_full[i]);
+        __syncwarp();
     };
     auto pv = [&](uint32_t i, uint32_t n, bool add) {
-        if (!bar_wait(&aux->p_full[i], p_uses[i]++ & 1, aux, p.ctl)) return false;
+        if (!warp_wait(&aux->p_full[i], p_uses[i]++ & 1, aux, p.ctl)) return false;
         tc_after();
         const uint64_t b = stage(n);
+        if (leader) {
 #pragma unroll
-        for (uint32_t k = 0; k < kTcBlock / 16; ++k)
-            mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b + k * (2048 >> 4), pv_desc, add || k > 0);
+            for (uint32_t k = 0; k < kTcBlock / 16; ++k)
+                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b + k * (2048 >> 4), pv_desc, add || k > 0);
+        }
+        __syncwarp();
         return true;
     };
     for (uint32_t parts = 0;; ++parts) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const uint32_t n = t.to - t.from;
         const bool two = t.rows > 128;
-        if (!bar_wait(&aux->q_full, parts & 1, aux, p.ctl)) return;
+        if (!warp_wait(&aux->q_full, parts & 1, aux, p.ctl)) return;
         tc_after();
         if (!full(kv)) return;
         qk(0, kv);
         if (two) qk(1, kv);
         release(kv);
-        if (n == 1) tc_commit(&aux->q_empty);
+        if (n == 1) commit(&aux->q_empty);
         for (uint32_t j = 0; j < n; ++j) {
             const uint32_t v = kv + 1, k = kv + 2;
             const bool more = j + 1 < n;
@@ -428,19 +448,19 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
                 if (!full(k)) return;
                 qk(0, k);
             } else {
-                tc_commit(&aux->o_full[0]);
+                commit(&aux->o_full[0]);
             }
             if (two) {
                 if (!pv(1, v, j > 0)) return;
                 release(v);
                 if (more) qk(1, k);
-                else tc_commit(&aux->o_full[1]);
+                else commit(&aux->o_full[1]);
             } else {
                 release(v);
             }
             if (more) {
                 release(k);
-                if (j + 2 == n) tc_commit(&aux->q_empty);
+                if (j + 2 == n) commit(&aux->q_empty);
             }
             kv += 2;
         }
@@ -597,7 +617,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t base = smem_u32(smem);
     TcAux *aux = reinterpret_cast<TcAux *>(smem + C::AUX_AT);
-    const uint32_t tid = threadIdx.x, warp = tid >> 5;
+    const uint32_t tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     TcDesc *desc = reinterpret_cast<TcDesc *>(p.desc) + blockIdx.x;
 
     if (tid == 0) {
@@ -649,11 +669,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         if (warp < 12) {
             load_role<DT, DP>(p, w, base, aux);
             cp_wait<0>();
-        } else if (tid == 12 * 32) {
+        } else if (warp == 12) {
             mma_role<DT, DP>(p, w, base, aux, tmem);
             // nothing of this CTA's is under way when it gives its memory back
-            tc_commit(&aux->drain);
-            bar_wait(&aux->drain, 0, aux, p.ctl);
+            __syncwarp();
+            if (elect_one()) tc_commit(&aux->drain);
+            warp_wait(&aux->drain, 0, aux, p.ctl);
         }
     }
     __syncwarp();
