@@ -246,6 +246,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
         if constexpr (DT == SZ_BF16) {
             constexpr uint32_t QL = DP / 8;
             const uint32_t c = tid % QL;
+#pragma unroll 4
             for (uint32_t r = tid / QL; r < q_rows; r += 128 / QL) {
                 const bool in = r < t.rows;
                 const uint32_t g = t.r0 + (in ? r : 0), i = div_by(g, p.group);
@@ -320,13 +321,21 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
                 }
                 const uint8_t *pool = (n & 1) ? p.cache.v : p.cache.k;
                 const uint32_t dst = base + C::RING_AT + (issued % C::STAGES) * C::STAGE + (piece / 8) * kPanel;
-#pragma unroll 8
-                for (uint32_t r = 0; r < 32; r += ROWS) {
-                    const uint64_t o = __shfl_sync(0xffffffffu, off, int(r + lane / LPR));
-                    const uint32_t row = row0 + r;
-                    const bool in = o != kBadOffset;
-                    if (has_piece)
-                        cp_async16(dst + row * 128 + (((piece % 8) ^ (row & 7)) << 4), pool + (in ? o + head_off : 0), in);
+                // eight rows' offsets at a time: one by one, the shuffles' latency bounds the copies
+#pragma unroll
+                for (uint32_t r = 0; r < 32; r += 8 * ROWS) {
+                    uint64_t o[8];
+#pragma unroll
+                    for (uint32_t u = 0; u < 8; ++u) o[u] = __shfl_sync(0xffffffffu, off, int(r + u * ROWS + lane / LPR));
+                    if (has_piece) {
+#pragma unroll
+                        for (uint32_t u = 0; u < 8; ++u) {
+                            const uint32_t row = row0 + r + u * ROWS;
+                            const bool in = o[u] != kBadOffset;
+                            cp_async16(dst + row * 128 + (((piece % 8) ^ (row & 7)) << 4),
+                                       pool + (in ? o[u] + head_off : 0), in);
+                        }
+                    }
                 }
                 cp_commit();
                 ++issued;
@@ -346,12 +355,15 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
                         id = page_id(j + 1);
                     }
                     const uint8_t *pool = (n & 1) ? p.cache.v : p.cache.k;
+                    uint64_t o[LPR];
 #pragma unroll
-                    for (uint32_t r = 0; r < 32; r += ROWS) {
-                        const uint64_t o = __shfl_sync(0xffffffffu, off, int(r + lane / LPR));
-                        const bool in = o != kBadOffset;
-                        if (has_piece)
-                            cp_async16(raw + (n % C::RAWS) * C::RAW + (r / ROWS) * 2048, pool + (in ? o + head_off : 0), in);
+                    for (uint32_t u = 0; u < LPR; ++u) o[u] = __shfl_sync(0xffffffffu, off, int(u * ROWS + lane / LPR));
+                    if (has_piece) {
+#pragma unroll
+                        for (uint32_t u = 0; u < LPR; ++u) {
+                            const bool in = o[u] != kBadOffset;
+                            cp_async16(raw + (n % C::RAWS) * C::RAW + u * 2048, pool + (in ? o[u] + head_off : 0), in);
+                        }
                     }
                 }
                 cp_commit();
@@ -491,6 +503,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
         if constexpr (DT == SZ_FP8_E5M2) sc *= __uint_as_float(uint32_t(127 - aux->exp[r]) << 23);
         __syncwarp();
         if ((threadIdx.x & 31) == 0) bar_arrive(&aux->q_empty);
+        __syncwarp();
         if (i == 0 || t.rows > 128) {
             Range rr{0, 0};
             if (r < t.rows) rr = token_range(p, t.s, div_by(t.r0 + r, p.group));
@@ -674,6 +687,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             // nothing of this CTA's is under way when it gives its memory back
             __syncwarp();
             if (elect_one()) tc_commit(&aux->drain);
+            __syncwarp();
             warp_wait(&aux->drain, 0, aux, p.ctl);
         }
     }
