@@ -6,7 +6,8 @@
 // pass over keys and values serves all query heads that share them.  A tile's
 // work is counted in blocks of BN places that any of its rows sees.  The
 // blocks of all tiles, in the order (KV head, sequence, tile, block), are dealt
-// out evenly: CTA c of C has blocks [c U / C, (c + 1) U / C).  A tile that
+// out evenly and in runs: CTA c of C has floor(U / C) of them, and one more if
+// c < U mod C.  A tile that
 // falls to several CTAs is joined from their partial results, in the order of
 // the CTAs, by the one that finishes last; so the result does not depend on
 // which one that is.
@@ -76,11 +77,16 @@ __device__ __forceinline__ uint32_t seq_tiles(const AttnParams &p, const SeqInfo
     return (s.q_len * p.group.d + TR - 1) / TR;
 }
 
+// Quotient and remainder; nearly always of numbers that fit 32 bits.
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+    return ((a | b) >> 32) == 0 ? uint64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 // Where a CTA stands in its share of the blocks.
 struct Work {
     uint64_t at, end;       // next block of the share, its end (global numbers)
-    uint64_t total;         // blocks in all
-    uint32_t ctas;          // CTAs that have a share
+    uint64_t each;          // blocks of a share ...
+    uint32_t more;          // ... and the number of CTAs, the first ones, that have one more
     uint32_t head, seq, tile;
     uint32_t from;          // the block of the tile at which `at` stands
 };
@@ -171,21 +177,29 @@ __device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w) {
         return run;
     };
     const uint64_t per_head = scan(false, 0);
-    w.total = per_head * p.cache.kv_heads;
-    w.ctas = w.total < gridDim.x ? uint32_t(w.total) : gridDim.x;
-    if (blockIdx.x >= w.ctas) return false;
-    w.at = w.total * blockIdx.x / w.ctas;
-    w.end = w.total * (blockIdx.x + 1) / w.ctas;
-    const uint64_t target = w.at % per_head;
+    const uint64_t total = per_head * p.cache.kv_heads;
+    w.each = quotient(total, gridDim.x);
+    w.more = uint32_t(total - w.each * gridDim.x);
+    w.at = w.each * blockIdx.x + min(blockIdx.x, w.more);
+    w.end = w.at + w.each + (blockIdx.x < w.more ? 1 : 0);
+    if (w.at == w.end) return false;
+    w.head = uint32_t(quotient(w.at, per_head));
+    const uint64_t target = w.at - w.head * per_head;
     if (chunks == 1) note(target);  // the one chunk is still at hand
     else scan(true, target);
     __syncthreads();
-    w.head = uint32_t(w.at / per_head);
     w.seq = s.found[0];
     w.tile = s.found[1];
     w.from = s.found[2];
     __syncthreads();
     return true;
+}
+
+// The CTA that has a block.
+__device__ __forceinline__ uint32_t work_owner(const Work &w, uint64_t block) {
+    const uint64_t longer = (w.each + 1) * w.more;
+    return block < longer ? uint32_t(quotient(block, w.each + 1))
+                          : w.more + uint32_t(quotient(block - longer, w.each));
 }
 
 // A CTA's part of a tile: blocks [from, to) of its n.
@@ -212,10 +226,9 @@ __device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w, ui
     if (t.from == 0 && t.to == t.n) {
         t.c_first = t.c_last = cta;
     } else {
-        // block x belongs to the last CTA c with floor(total c / ctas) <= x
-        const uint64_t x0 = w.at - w.from, x1 = x0 + t.n - 1;
-        t.c_first = uint32_t(((x0 + 1) * w.ctas - 1) / w.total);
-        t.c_last = uint32_t(((x1 + 1) * w.ctas - 1) / w.total);
+        const uint64_t x0 = w.at - w.from;
+        t.c_first = work_owner(w, x0);
+        t.c_last = work_owner(w, x0 + t.n - 1);
     }
     return t;
 }

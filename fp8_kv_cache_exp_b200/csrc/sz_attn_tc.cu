@@ -9,10 +9,12 @@
 // bits, and 128 columns of sums.  The roles:
 //   warps 0-3, 4-7  softmax of the first and the second tile, a thread a row:
 //                   a row's maximum and sum need no exchange between threads
-//   warps 8-11      keys, values and queries into shared memory
+//   warps 8-11      keys and values into shared memory
 //   warp 12         issues the products: per block p0 v, q0 k', p1 v, q1 k', so
 //                   that the tensor cores work on one tile while the other's
 //                   softmax runs
+//   warps 13-15     queries into shared memory: a tile's as soon as its last
+//                   product with the ones before is done
 // m is the largest score so far only to within 2^kSlack: the sums are rescaled
 // (through registers) when a row's maximum has grown by more, so that most
 // blocks leave them where they are.
@@ -65,7 +67,7 @@ struct TcCfg {
 
 struct TcAux {
     uint64_t full[8], empty[8];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t drain;
     uint32_t tmem, abort, bad;
@@ -208,14 +210,14 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 
 // ------------------------------------------------------------------- roles
 
-// Keys, values and queries into shared memory (warps 8-11).
+// Keys and values into shared memory (warps 8-11).
 template <int DT, int DP>
 __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t LPR = DP * C::EB / 16;  // lanes to a row of the cache
     constexpr uint32_t ROWS = 32 / LPR;
     const uint32_t tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
-    const uint32_t d = p.cache.head_dim, G = p.group.d;
+    const uint32_t d = p.cache.head_dim;
     const uint32_t piece = lane % LPR, row0 = warp * 32 + lane / LPR;
     const bool has_piece = piece * 16 < d * C::EB;
     // tiles of keys and values, in the order in which they are used; what is behind `ready` has been handed over
@@ -232,62 +234,11 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
     auto wait_free = [&](uint32_t n) {
         return n < C::STAGES || warp_wait(&aux->empty[n % C::STAGES], (n / C::STAGES - 1) & 1, aux, p.ctl);
     };
-    for (uint32_t parts = 0;; ++parts) {
+    for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const int32_t *ids = p.cache.table + uint64_t(w.seq) * p.cache.table_stride;
         const uint32_t part_hi = min((t.block0 + t.to) * kTcBlock, t.r.hi);
         const uint64_t head_off = uint64_t(w.head) * d * C::EB + piece * 16;
-
-        // queries, once the last part's products with them are done
-        if (parts > 0) {
-            if (!warp_wait(&aux->q_empty, (parts - 1) & 1, aux, p.ctl)) return;
-        }
-        const uint32_t q_rows = t.rows > 128 ? 256 : 128;
-        if constexpr (DT == SZ_BF16) {
-            constexpr uint32_t QL = DP / 8;
-            const uint32_t c = tid % QL;
-#pragma unroll 4
-            for (uint32_t r = tid / QL; r < q_rows; r += 128 / QL) {
-                const bool in = r < t.rows;
-                const uint32_t g = t.r0 + (in ? r : 0), i = div_by(g, p.group);
-                const uint8_t *src = p.q.p + uint64_t(t.s.q0 + i) * p.q.ts + uint64_t(w.head * G + (g - i * G)) * p.q.hs;
-                const uint32_t dst = base + (r / 128) * C::STAGE + (c / 8) * kPanel + (r % 128) * 128 +
-                                     (((c % 8) ^ (r & 7)) << 4);
-                if (c * 8 < d) cp_async16(dst, src + c * 16, in);
-            }
-            cp_commit();
-            cp_wait<0>();
-            hand_over(issued);
-        } else {
-            constexpr uint32_t QL = DP / 8;
-            const uint32_t c = tid % QL;
-#pragma unroll 4
-            for (uint32_t r = tid / QL; r < q_rows; r += 128 / QL) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < t.rows && c * 8 < d) {
-                    const uint32_t i = div_by(t.r0 + r, p.group);
-                    v = *reinterpret_cast<const uint4 *>(p.q.p + uint64_t(t.s.q0 + i) * p.q.ts +
-                                                         uint64_t(w.head * G + (t.r0 + r - i * G)) * p.q.hs + c * 16);
-                }
-                uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                float top = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
-#pragma unroll
-                for (int o = QL / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                int e = 0;
-                if (top > 0.f && top < INFINITY) e = min(13 - (int(__float_as_uint(top) >> 23) - 127), 120);
-                const float up = __uint_as_float(uint32_t(127 + e) << 23);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = pack_f16(bf16_lo(x[j]) * up, bf16_hi(x[j]) * up);
-                if (c * 8 < d)
-                    sts_u128(base + (r / 128) * C::STAGE + (c / 8) * kPanel + (r % 128) * 128 + (((c % 8) ^ (r & 7)) << 4),
-                             make_uint4(x[0], x[1], x[2], x[3]));
-                if (c == 0) aux->exp[r] = int8_t(e);
-            }
-        }
-        fence_proxy_async_smem();
-        bar_arrive(&aux->q_full);
 
         // the place of this lane's row of a block, and its page's id
         auto place = [&](uint32_t j) { return (t.block0 + j) * kTcBlock + warp * 32 + lane; };
@@ -395,6 +346,80 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
     }
 }
 
+// Queries into shared memory (warps 13-15).
+constexpr uint32_t kQueryWarps = 3;
+template <int DT, int DP>
+__device__ __forceinline__ void query_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux) {
+    using C = TcCfg<DT, DP>;
+    constexpr uint32_t QL = DP / 8, QR = 32 / QL;          // lanes to a row, rows to an instruction
+    constexpr uint32_t BATCH = DT == SZ_BF16 ? 8 : 4;      // instructions under way at a time
+    const uint32_t lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 13, c = lane % QL;
+    const uint32_t d = p.cache.head_dim, G = p.group.d;
+    uint32_t uses[2] = {0, 0};
+    for (;;) {
+        const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
+        const uint8_t *q = p.q.p + uint64_t(t.s.q0) * p.q.ts + uint64_t(w.head * G) * p.q.hs;
+        for (uint32_t i = 0; i * 128 < t.rows; ++i) {
+            if (uses[i] > 0 && !warp_wait(&aux->q_empty[i], (uses[i] - 1) & 1, aux, p.ctl)) return;
+            ++uses[i];
+            const uint32_t tile = base + i * C::STAGE + (c / 8) * kPanel;
+            for (uint32_t r0 = warp * BATCH * QR; r0 < 128; r0 += kQueryWarps * BATCH * QR) {
+                // a lane finds one row; rows behind the last are zeros
+                const uint32_t mine = i * 128 + r0 + lane % (BATCH * QR);
+                uint64_t at = kBadOffset;
+                if (mine < t.rows) {
+                    const uint32_t g = t.r0 + mine, tok = div_by(g, p.group);
+                    at = uint64_t(tok) * p.q.ts + uint64_t(g - tok * G) * p.q.hs;
+                }
+                uint64_t o[BATCH];
+#pragma unroll
+                for (uint32_t u = 0; u < BATCH; ++u) o[u] = __shfl_sync(0xffffffffu, at, int(u * QR + lane / QL));
+                if constexpr (DT == SZ_BF16) {
+                    if (c * 8 < d) {
+#pragma unroll
+                        for (uint32_t u = 0; u < BATCH; ++u) {
+                            const uint32_t r = r0 + u * QR + lane / QL;
+                            const bool in = o[u] != kBadOffset;
+                            cp_async16(tile + r * 128 + (((c % 8) ^ (r & 7)) << 4), in ? q + o[u] + c * 16 : p.q.p, in);
+                        }
+                    }
+                } else {
+                    uint4 v[BATCH];
+#pragma unroll
+                    for (uint32_t u = 0; u < BATCH; ++u) {
+                        v[u] = make_uint4(0, 0, 0, 0);
+                        if (o[u] != kBadOffset && c * 8 < d) v[u] = *reinterpret_cast<const uint4 *>(q + o[u] + c * 16);
+                    }
+#pragma unroll
+                    for (uint32_t u = 0; u < BATCH; ++u) {
+                        const uint32_t r = r0 + u * QR + lane / QL;
+                        uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                        float top = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
+#pragma unroll
+                        for (int s = QL / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                        int e = 0;
+                        if (top > 0.f && top < INFINITY) e = min(13 - (int(__float_as_uint(top) >> 23) - 127), 120);
+                        const float up = __uint_as_float(uint32_t(127 + e) << 23);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[j] = pack_f16(bf16_lo(x[j]) * up, bf16_hi(x[j]) * up);
+                        if (c * 8 < d)
+                            sts_u128(tile + r * 128 + (((c % 8) ^ (r & 7)) << 4), make_uint4(x[0], x[1], x[2], x[3]));
+                        if (c == 0) aux->exp[i * 128 + r] = int8_t(e);
+                    }
+                }
+            }
+            cp_commit();
+            cp_wait<0>();
+            fence_proxy_async_smem();
+            bar_arrive(&aux->q_full[i]);
+            __syncwarp();
+        }
+        if (!work_next<kTcRows>(p, w, t)) return;
+    }
+}
+
 // The products.  The warp goes through the loop together and one elected lane
 // issues: behind a test of the thread's own number the compiler does not see
 // that one lane is left, and each product took twice as long.
@@ -404,7 +429,7 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
     const uint32_t d = p.cache.head_dim, ksteps = d / 16;
     const uint32_t qk_desc = instr_desc(DT, kTcBlock, false), pv_desc = instr_desc(DT, d, true);
     const bool leader = elect_one();
-    uint32_t kv = 0, p_uses[2] = {0, 0};
+    uint32_t kv = 0, p_uses[2] = {0, 0}, q_uses[2] = {0, 0};
     auto full = [&](uint32_t n) {
         const bool ok = warp_wait(&aux->full[n % C::STAGES], (n / C::STAGES) & 1, aux, p.ctl);
         tc_after();
@@ -440,17 +465,25 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
         __syncwarp();
         return true;
     };
-    for (uint32_t parts = 0;; ++parts) {
+    auto queries = [&](uint32_t i) {
+        const bool ok = warp_wait(&aux->q_full[i], q_uses[i]++ & 1, aux, p.ctl);
+        tc_after();
+        return ok;
+    };
+    for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const uint32_t n = t.to - t.from;
         const bool two = t.rows > 128;
-        if (!warp_wait(&aux->q_full, parts & 1, aux, p.ctl)) return;
-        tc_after();
         if (!full(kv)) return;
+        if (!queries(0)) return;
         qk(0, kv);
-        if (two) qk(1, kv);
+        if (n == 1) commit(&aux->q_empty[0]);
+        if (two) {
+            if (!queries(1)) return;
+            qk(1, kv);
+            if (n == 1) commit(&aux->q_empty[1]);
+        }
         release(kv);
-        if (n == 1) commit(&aux->q_empty);
         for (uint32_t j = 0; j < n; ++j) {
             const uint32_t v = kv + 1, k = kv + 2;
             const bool more = j + 1 < n;
@@ -459,21 +492,23 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
             if (more) {
                 if (!full(k)) return;
                 qk(0, k);
+                if (j + 2 == n) commit(&aux->q_empty[0]);
             } else {
                 commit(&aux->o_full[0]);
             }
             if (two) {
                 if (!pv(1, v, j > 0)) return;
                 release(v);
-                if (more) qk(1, k);
-                else commit(&aux->o_full[1]);
+                if (more) {
+                    qk(1, k);
+                    if (j + 2 == n) commit(&aux->q_empty[1]);
+                } else {
+                    commit(&aux->o_full[1]);
+                }
             } else {
                 release(v);
             }
-            if (more) {
-                release(k);
-                if (j + 2 == n) commit(&aux->q_empty);
-            }
+            if (more) release(k);
             kv += 2;
         }
         if (!work_next<kTcRows>(p, w, t)) return;
@@ -488,28 +523,27 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
     const uint32_t lanes = (threadIdx.x & 96) << 16;  // the warp's quarter of tensor memory
     const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * 128;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    uint32_t s_uses = 0, o_uses = 0;
-    for (uint32_t parts = 0;; ++parts) {
+    uint32_t q_uses = 0, s_uses = 0, o_uses = 0;
+    for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const bool whole_tile = t.c_first == t.c_last;
         if (threadIdx.x == 0 && !whole_tile && t.c_first == blockIdx.x) {
             desc->join = w;
             desc->joins = 1;
         }
-        // every warp sees every part's queries come, whether it has rows or not: their next ones wait for it
-        const uint32_t r = i * 128 + row;
-        if (!warp_wait(&aux->q_full, parts & 1, aux, p.ctl)) return;
-        float sc = p.scale_log2;
-        if constexpr (DT == SZ_FP8_E5M2) sc *= __uint_as_float(uint32_t(127 - aux->exp[r]) << 23);
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) bar_arrive(&aux->q_empty);
-        __syncwarp();
         if (i == 0 || t.rows > 128) {
+            const uint32_t r = i * 128 + row;
             Range rr{0, 0};
             if (r < t.rows) rr = token_range(p, t.s, div_by(t.r0 + r, p.group));
             // every row of the 128 sees [full_lo, full_hi)
             const uint32_t full_hi = token_range(p, t.s, div_by(t.r0 + i * 128, p.group)).hi;
             const uint32_t full_lo = token_range(p, t.s, div_by(t.r0 + min(i * 128 + 128, t.rows) - 1, p.group)).lo;
+            if (!warp_wait(&aux->q_full[i], q_uses++ & 1, aux, p.ctl)) return;
+            float sc = p.scale_log2;
+            if constexpr (DT == SZ_FP8_E5M2) sc *= __uint_as_float(uint32_t(127 - aux->exp[r]) << 23);
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) bar_arrive(&aux->q_empty[i]);
+            __syncwarp();
             float m = -INFINITY, l = 0.f;
             for (uint32_t j = t.from; j < t.to; ++j) {
                 if (!warp_wait(&aux->s_full[i], s_uses++ & 1, aux, p.ctl)) return;
@@ -638,9 +672,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(&aux->full[i], 128);
             mbar_init(&aux->empty[i], 1);
         }
-        mbar_init(&aux->q_full, 128);
-        mbar_init(&aux->q_empty, 1 + 8);  // the products, and the softmax's warps
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&aux->q_full[i], 32 * kQueryWarps);
+            mbar_init(&aux->q_empty[i], 1 + 4);  // the products, and the warps of the tile's softmax
             mbar_init(&aux->s_full[i], 1);
             mbar_init(&aux->p_full[i], 128);
             mbar_init(&aux->o_full[i], 1);
@@ -689,6 +723,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             if (elect_one()) tc_commit(&aux->drain);
             __syncwarp();
             warp_wait(&aux->drain, 0, aux, p.ctl);
+        } else {
+            query_role<DT, DP>(p, w, base, aux);
+            cp_wait<0>();
         }
     }
     __syncwarp();
@@ -701,16 +738,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 
 // ------------------------------------------------------------------ joining
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;
 constexpr int kJoinSlices = kTcRows / kJoinRows;
+constexpr uint32_t kJoinWarps = kJoinThreads / 32;
+constexpr uint32_t kJoinSplit = 4;                        // groups of columns ...
+constexpr uint32_t kJoinGroups = kJoinWarps / kJoinSplit; // ... and of parts
 
 // CTA (c, slice): 32 rows of the tile that CTA c began and others ended, a lane
-// a row, a quarter of the columns to a warp.
+// a row; a warp has a quarter of the columns of every second part.
 template <int DT, int DP>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p) {
     using C = TcCfg<DT, DP>;
-    __shared__ float s_f[kMaxSms][kJoinRows];
+    constexpr uint32_t COLS = DP / kJoinSplit;
+    __shared__ float s_o[kJoinGroups - 1][DP][kJoinRows];
+    __shared__ float s_m[kJoinWarps][kJoinRows], s_l[kJoinWarps][kJoinRows];
     __shared__ uint32_t s_bad;
     pdl_wait();
     pdl_launch_dependents();
@@ -728,42 +770,67 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             auto slot = [&](uint32_t k) {
                 return p.part + uint64_t(part_slot(t.c_first + k, t)) * kTcRows * (d + 2) + r;
             };
-            float M = -INFINITY, L = 0.f;
-            for (uint32_t k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(slot(k) + d * kTcRows));
+            // the largest m of all parts, and sum l against it
+            float M = -INFINITY;
+            for (uint32_t k = warp; k < parts; k += kJoinWarps) M = fmaxf(M, __ldcg(slot(k) + d * kTcRows));
+            s_m[warp][lane] = M;
+            __syncthreads();
+#pragma unroll
+            for (uint32_t k = 0; k < kJoinWarps; ++k) M = fmaxf(M, s_m[k][lane]);
             const float safe = M == -INFINITY ? 0.f : M;
-            for (uint32_t k = 0; k < parts; ++k) {
+            float L = 0.f;
+            for (uint32_t k = warp; k < parts; k += kJoinWarps)
+                L = fmaf(exp2_fast(__ldcg(slot(k) + d * kTcRows) - safe), __ldcg(slot(k) + (d + 1) * kTcRows), L);
+            s_l[warp][lane] = L;
+            const uint32_t col0 = (warp % kJoinSplit) * (d / kJoinSplit), kg = warp / kJoinSplit;
+            float v[COLS];
+#pragma unroll
+            for (uint32_t e = 0; e < COLS; ++e) v[e] = 0.f;
+            for (uint32_t k = kg; k < parts; k += kJoinGroups) {
                 const float f = exp2_fast(__ldcg(slot(k) + d * kTcRows) - safe);
-                if (warp == 0) s_f[k][lane] = f;
-                L += f * __ldcg(slot(k) + (d + 1) * kTcRows);
+                const float *from = slot(k) + col0 * kTcRows;
+#pragma unroll
+                for (uint32_t e = 0; e < COLS; ++e)
+                    if (e < d / kJoinSplit) v[e] = fmaf(f, __ldcg(from + e * kTcRows), v[e]);
+            }
+            if (kg > 0) {
+#pragma unroll
+                for (uint32_t e = 0; e < COLS; ++e)
+                    if (e < d / kJoinSplit) s_o[kg - 1][col0 + e][lane] = v[e];
             }
             __syncthreads();
             const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs;
-            float worst = 0.f;
-            for (uint32_t e = warp * (d / 4); e < (warp + 1) * (d / 4); e += 4) {
-                float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-                for (uint32_t k = 0; k < parts; ++k) {
-                    const float f = s_f[k][lane];
+            if (kg == 0) {
+                L = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = fmaf(f, __ldcg(slot(k) + (e + j) * kTcRows), v[j]);
-                }
+                for (uint32_t k = 0; k < kJoinWarps; ++k) L += s_l[k][lane];
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs + 2 * col0;
+                float worst = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[j] *= inv;
-                    worst = fmaf(0.f, v[j], worst);
+                for (uint32_t e = 0; e < COLS; e += 4) {
+                    if (e >= d / kJoinSplit) break;
+#pragma unroll
+                    for (uint32_t j = e; j < e + 4; ++j) {
+#pragma unroll
+                        for (uint32_t k = 0; k < kJoinGroups - 1; ++k) v[j] += s_o[k][col0 + j][lane];
+                        v[j] *= inv;
+                        worst = fmaf(0.f, v[j], worst);  // stays 0, or is NaN
+                    }
+                    if (r < t.rows)
+                        *reinterpret_cast<uint2 *>(out + 2 * e) =
+                            make_uint2(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]));
                 }
-                if (r < t.rows)
-                    *reinterpret_cast<uint2 *>(out + 2 * e) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                if (warp == 0 && r < t.rows && p.lse)
+                    p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] =
+                        L == 0.f ? -INFINITY : kLn2 * (M - C::RAISE + log2f(L));
+                if (r < t.rows && worst != 0.f) atomicOr(&s_bad, 1u << lane);
             }
-            if (warp == 0 && r < t.rows && p.lse)
-                p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] = L == 0.f ? -INFINITY : kLn2 * (M - C::RAISE + log2f(L));
-            if (r < t.rows && worst != 0.f) atomicOr(&s_bad, 1u << lane);
             __syncthreads();
-            for (uint32_t bad = s_bad, k = 0; bad; bad &= bad - 1, ++k) {
+            uint32_t k = 0;
+            for (uint32_t bad = s_bad; bad; bad &= bad - 1, ++k) {
                 const uint32_t x = __ffs(bad) - 1;
-                if (k % (kJoinThreads / 32) == warp)
+                if (k % kJoinWarps == warp)
                     repair_row<DT>(p, t.s, w.seq, w.head, t.r0 + slice * kJoinRows + x, t.r);
             }
         }
