@@ -4,23 +4,24 @@
 //   x = scale * q . k,  p = exp(x - m),  o = sum p v / sum p
 //
 // A CTA takes 256 rows of one sequence and KV head, as two tiles of 128, and
-// goes over their places in blocks of 128.  Scores, p and the sums of p v stay
-// in tensor memory: per tile 128 columns of scores, which p overwrites in 16
-// bits, and 128 columns of sums.  The roles:
+// goes over their places in blocks of 64.  Scores, p and the sums of p v stay
+// in tensor memory: per tile two buffers of 64 columns of scores, which p
+// overwrites in 16 bits, and 128 columns of sums.  The roles:
 //   warps 0-3, 4-7  softmax of the first and the second tile, a thread a row:
 //                   a row's maximum and sum need no exchange between threads
 //   warps 8-11      keys and values into shared memory
-//   warp 12         issues the products: per block p0 v, q0 k', p1 v, q1 k', so
-//                   that the tensor cores work on one tile while the other's
-//                   softmax runs
+//   warp 12         issues the products: for each block and tile p v, then q k'
+//                   of the block after the next into the buffer that is free
+//                   now, so that a softmax finds its next scores ready
 //   warps 13-15     queries into shared memory: a tile's as soon as its last
 //                   product with the ones before is done
-// m is the largest score so far only to within 2^kSlack: the sums are rescaled
+// m is the largest score so far only to within 2^SLACK: the sums are rescaled
 // (through registers) when a row's maximum has grown by more, so that most
 // blocks leave them where they are.
 //
-// What bounds it: a block of 256 rows and heads of 128 is 2048 clocks of matrix
-// products and 2048 clocks of ex2 (16 a clock).
+// What bounds it: 128 places of 256 rows and heads of 128 are 2048 clocks of
+// ex2 (16 a clock) and 2560 of matrix products (q k' of 64 columns reads 6 KB
+// of shared memory in what would be 32 clocks, and takes 48).
 //
 // The cache's pages are of any size and lie anywhere, so rows are fetched one by
 // one, by 16-byte asynchronous copies into the swizzled layout that the products
@@ -39,22 +40,24 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;
-constexpr int kTcBlock = 128;
-constexpr uint32_t kPanel = 128 * 128;  // bytes of 128 rows of 64 16-bit elements
-// registers of a softmax thread and of the others: 256 * 200 + 256 * 56 = 512 * 128,
+constexpr int kTcBlock = 64;
+constexpr uint32_t kQPanel = 128 * 128;       // bytes of 128 rows of 64 16-bit elements
+constexpr uint32_t kPanel = kTcBlock * 128;   // of a block's rows
+// registers of a softmax thread and of the others: 256 * 152 + 256 * 104 = 512 * 128,
 // what the CTA is launched with
-#define SZ_TC_REGS_SOFTMAX "200"
-#define SZ_TC_REGS_OTHER "56"
+#define SZ_TC_REGS_SOFTMAX "152"
+#define SZ_TC_REGS_OTHER "104"
 
 template <int DT, int DP>
 struct TcCfg {
     static constexpr uint32_t EB = DT == SZ_BF16 ? 2 : 1;
     static constexpr uint32_t PANELS = DP / 64;
-    static constexpr uint32_t STAGE = PANELS * kPanel;       // 128 rows
-    static constexpr uint32_t STAGES = DP == 64 ? 6 : (DT == SZ_BF16 ? 5 : 4);
-    static constexpr uint32_t RAW = 128 * DP;                // E5M2: 128 rows as they come
-    static constexpr uint32_t RAWS = DT == SZ_BF16 ? 0 : (DP == 64 ? 4 : 2);
-    static constexpr uint32_t RING_AT = 2 * STAGE;           // behind the queries
+    static constexpr uint32_t QTILE = PANELS * kQPanel;
+    static constexpr uint32_t STAGE = PANELS * kPanel;       // a block's keys or values
+    static constexpr uint32_t STAGES = DT == SZ_BF16 ? 10 : 6;
+    static constexpr uint32_t RAW = kTcBlock * DP;           // E5M2: as they come
+    static constexpr uint32_t RAWS = DT == SZ_BF16 ? 0 : 8;
+    static constexpr uint32_t RING_AT = 2 * QTILE;           // behind the queries
     static constexpr uint32_t RAW_AT = RING_AT + STAGES * STAGE;
     static constexpr uint32_t AUX_AT = RAW_AT + RAWS * RAW;
     static constexpr uint32_t SMEM = AUX_AT + 1024 + 1024;   // barriers and exponents; slack to align the base
@@ -66,9 +69,10 @@ struct TcCfg {
 };
 
 struct TcAux {
-    uint64_t full[8], empty[8];
+    uint64_t full[10], empty[10];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2][2], p_full[2][2];  // of a tile's buffers
+    uint64_t o_done[2], o_last[2];        // a tile's product with values is done; its last of the part
     uint64_t drain;
     uint32_t tmem, abort, bad;
     int8_t exp[kTcRows];  // E5M2: exponent taken out of each query row
@@ -163,8 +167,9 @@ __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t *r) {
 }
 
 // Shared-memory descriptor of rows of 128 bytes, 8 rows to a swizzle atom:
-// leading offset (from one 64-element panel to the next, where the matrix runs
-// along the row), stride offset of 1024 bytes from 8 rows to the next.
+// leading offset (from one 64-element panel to the next; only values, whose
+// rows run along the result's columns, have a use for it), stride offset of
+// 1024 bytes from 8 rows to the next.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t a) {
     return uint64_t((a >> 4) & 0x3fff) | uint64_t(kPanel >> 4) << 16 | uint64_t(1024 >> 4) << 32 | 1ull << 46 |
            2ull << 61;
@@ -210,22 +215,24 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 
 // ------------------------------------------------------------------- roles
 
-// Keys and values into shared memory (warps 8-11).
+// Keys and values into shared memory (warps 8-11), in the order in which they
+// are used: k0, k1, v0, k2, v1, ...
 template <int DT, int DP>
 __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t LPR = DP * C::EB / 16;  // lanes to a row of the cache
-    constexpr uint32_t ROWS = 32 / LPR;
+    constexpr uint32_t ROWS = 32 / LPR;        // rows to an instruction
+    constexpr uint32_t N = 16 / ROWS;          // instructions to a warp's 16 rows of a block
     const uint32_t tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
     const uint32_t d = p.cache.head_dim;
-    const uint32_t piece = lane % LPR, row0 = warp * 32 + lane / LPR;
+    const uint32_t piece = lane % LPR, row0 = warp * 16 + lane / LPR;
     const bool has_piece = piece * 16 < d * C::EB;
-    // tiles of keys and values, in the order in which they are used; what is behind `ready` has been handed over
-    uint32_t issued = 0, ready = 0;
+    uint32_t issued = 0, ready = 0;  // what is behind `ready` has been handed over
     auto hand_over = [&](uint32_t to) {
         if (ready == to) return;
         fence_proxy_async_smem();
         for (; ready < to; ++ready) bar_arrive(&aux->full[ready % C::STAGES]);
+        __syncwarp();
     };
     auto stage_free = [&](uint32_t n) {
         if (n < C::STAGES) return true;
@@ -241,7 +248,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
         const uint64_t head_off = uint64_t(w.head) * d * C::EB + piece * 16;
 
         // the place of this lane's row of a block, and its page's id
-        auto place = [&](uint32_t j) { return (t.block0 + j) * kTcBlock + warp * 32 + lane; };
+        auto place = [&](uint32_t j) { return (t.block0 + j) * kTcBlock + warp * 16 + (lane & 15); };
         auto page_id = [&](uint32_t j) -> int32_t {
             const uint32_t at = place(j);
             return j < t.to && at >= t.r.lo && at < part_hi ? __ldg(ids + div_by(at, p.cache.page_tokens)) : 0;
@@ -256,82 +263,83 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
             }
             return uint64_t(id) * p.cache.page_bytes + uint64_t(at - page * p.cache.page_tokens.d) * p.cache.row_bytes;
         };
-        int32_t id = page_id(t.from);
-        uint64_t off = 0;
-        if constexpr (DT == SZ_BF16) {
-            for (uint32_t n = 0; n < 2 * (t.to - t.from); ++n) {
-                const uint32_t j = t.from + n / 2;
-                if ((n & 1) == 0) {
-                    off = offset(j, id);
-                    id = page_id(j + 1);
+        // Offsets of all of a lane's rows first: one by one, the shuffles' latency
+        // bounds the copies.
+        auto copy = [&](const uint8_t *pool, uint64_t off, auto &&to) {
+            uint64_t o[N];
+#pragma unroll
+            for (uint32_t u = 0; u < N; ++u) o[u] = __shfl_sync(0xffffffffu, off, int(u * ROWS + lane / LPR));
+            if (has_piece) {
+#pragma unroll
+                for (uint32_t u = 0; u < N; ++u) {
+                    const bool in = o[u] != kBadOffset;
+                    cp_async16(to(u), pool + (in ? o[u] + head_off : 0), in);
                 }
+            }
+            cp_commit();
+        };
+        const uint32_t blocks = t.to - t.from, tiles = 2 * blocks;
+        int32_t id = page_id(t.from);
+        uint64_t k_off = offset(t.from, id), v_off[2] = {0, 0};  // of the next keys' block, and of the next values' two
+        id = page_id(t.from + 1);
+        uint32_t k_next = 0;
+        // the next tile in order: keys if they are not a block ahead of the values
+        auto next_copy = [&](uint32_t n, auto &&to) {
+            const bool key = n == 0 || ((n & 1) && k_next < blocks);
+            if (key) {
+                copy(p.cache.k, k_off, to);
+                if (n == 0) v_off[0] = k_off;
+                else v_off[1] = k_off;
+                ++k_next;
+            } else {
+                copy(p.cache.v, v_off[0], to);
+                v_off[0] = v_off[1];
+            }
+            if (key && k_next < blocks) {
+                k_off = offset(t.from + k_next, id);
+                id = page_id(t.from + k_next + 1);
+            }
+        };
+        if constexpr (DT == SZ_BF16) {
+            for (uint32_t n = 0; n < tiles; ++n) {
                 if (!stage_free(issued)) {
                     cp_wait<0>();
                     hand_over(issued);
                     if (!wait_free(issued)) return;
                 }
-                const uint8_t *pool = (n & 1) ? p.cache.v : p.cache.k;
                 const uint32_t dst = base + C::RING_AT + (issued % C::STAGES) * C::STAGE + (piece / 8) * kPanel;
-                // eight rows' offsets at a time: one by one, the shuffles' latency bounds the copies
-#pragma unroll
-                for (uint32_t r = 0; r < 32; r += 8 * ROWS) {
-                    uint64_t o[8];
-#pragma unroll
-                    for (uint32_t u = 0; u < 8; ++u) o[u] = __shfl_sync(0xffffffffu, off, int(r + u * ROWS + lane / LPR));
-                    if (has_piece) {
-#pragma unroll
-                        for (uint32_t u = 0; u < 8; ++u) {
-                            const uint32_t row = row0 + r + u * ROWS;
-                            const bool in = o[u] != kBadOffset;
-                            cp_async16(dst + row * 128 + (((piece % 8) ^ (row & 7)) << 4),
-                                       pool + (in ? o[u] + head_off : 0), in);
-                        }
-                    }
-                }
-                cp_commit();
+                next_copy(n, [&](uint32_t u) {
+                    const uint32_t row = row0 + u * ROWS;
+                    return dst + row * 128 + (((piece % 8) ^ (row & 7)) << 4);
+                });
                 ++issued;
-                cp_wait<2>();
-                if (issued > 2) hand_over(max(ready, issued - 2));
+                cp_wait<4>();
+                if (issued > ready + 4) hand_over(issued - 4);
             }
             cp_wait<0>();
             hand_over(issued);
         } else {
-            const uint32_t tiles = 2 * (t.to - t.from);
             const uint32_t raw = base + C::RAW_AT + tid * 16;
             for (uint32_t n = 0; n < tiles + C::RAWS - 1; ++n) {
-                if (n < tiles) {
-                    const uint32_t j = t.from + n / 2;
-                    if ((n & 1) == 0) {
-                        off = offset(j, id);
-                        id = page_id(j + 1);
-                    }
-                    const uint8_t *pool = (n & 1) ? p.cache.v : p.cache.k;
-                    uint64_t o[LPR];
-#pragma unroll
-                    for (uint32_t u = 0; u < LPR; ++u) o[u] = __shfl_sync(0xffffffffu, off, int(u * ROWS + lane / LPR));
-                    if (has_piece) {
-#pragma unroll
-                        for (uint32_t u = 0; u < LPR; ++u) {
-                            const bool in = o[u] != kBadOffset;
-                            cp_async16(raw + (n % C::RAWS) * C::RAW + u * 2048, pool + (in ? o[u] + head_off : 0), in);
-                        }
-                    }
-                }
-                cp_commit();
+                if (n < tiles) next_copy(n, [&](uint32_t u) { return raw + (n % C::RAWS) * C::RAW + u * 2048; });
+                else cp_commit();
                 if (n + 1 < C::RAWS) continue;
                 const uint32_t m = n + 1 - C::RAWS;  // the tile that has come
+                if (m >= tiles) continue;
                 cp_wait<C::RAWS - 1>();
                 if (!wait_free(issued)) return;
                 const uint32_t dst = base + C::RING_AT + (issued % C::STAGES) * C::STAGE + (piece / 4) * kPanel;
                 if (has_piece) {
+                    uint4 v[N];
 #pragma unroll
-                    for (uint32_t r = 0; r < 32; r += ROWS) {
-                        const uint4 v = lds_u128(raw + (m % C::RAWS) * C::RAW + (r / ROWS) * 2048);
-                        const uint4 lo = make_uint4(prmt(v.x, 0, 0x1404), prmt(v.x, 0, 0x3424), prmt(v.y, 0, 0x1404),
-                                                    prmt(v.y, 0, 0x3424));
-                        const uint4 hi = make_uint4(prmt(v.z, 0, 0x1404), prmt(v.z, 0, 0x3424), prmt(v.w, 0, 0x1404),
-                                                    prmt(v.w, 0, 0x3424));
-                        const uint32_t row = row0 + r, a = dst + row * 128, ch = 2 * (piece % 4);
+                    for (uint32_t u = 0; u < N; ++u) v[u] = lds_u128(raw + (m % C::RAWS) * C::RAW + u * 2048);
+#pragma unroll
+                    for (uint32_t u = 0; u < N; ++u) {
+                        const uint4 lo = make_uint4(prmt(v[u].x, 0, 0x1404), prmt(v[u].x, 0, 0x3424),
+                                                    prmt(v[u].y, 0, 0x1404), prmt(v[u].y, 0, 0x3424));
+                        const uint4 hi = make_uint4(prmt(v[u].z, 0, 0x1404), prmt(v[u].z, 0, 0x3424),
+                                                    prmt(v[u].w, 0, 0x1404), prmt(v[u].w, 0, 0x3424));
+                        const uint32_t row = row0 + u * ROWS, a = dst + row * 128, ch = 2 * (piece % 4);
                         // the lanes of the second panel go the other way round, off the first one's banks
                         const bool odd = piece >= 4;
                         sts_u128(a + (((ch + (odd ? 1 : 0)) ^ (row & 7)) << 4), odd ? hi : lo);
@@ -341,6 +349,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
                 ++issued;
                 hand_over(issued);
             }
+            cp_wait<0>();
         }
         if (!work_next<kTcRows>(p, w, t)) return;
     }
@@ -352,17 +361,20 @@ template <int DT, int DP>
 __device__ __forceinline__ void query_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t QL = DP / 8, QR = 32 / QL;          // lanes to a row, rows to an instruction
-    constexpr uint32_t BATCH = DT == SZ_BF16 ? 8 : 4;      // instructions under way at a time
+    constexpr uint32_t BATCH = 8;
     const uint32_t lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 13, c = lane % QL;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    uint32_t uses[2] = {0, 0};
+    uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i]
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const uint8_t *q = p.q.p + uint64_t(t.s.q0) * p.q.ts + uint64_t(w.head * G) * p.q.hs;
         for (uint32_t i = 0; i * 128 < t.rows; ++i) {
-            if (uses[i] > 0 && !warp_wait(&aux->q_empty[i], (uses[i] - 1) & 1, aux, p.ctl)) return;
-            ++uses[i];
-            const uint32_t tile = base + i * C::STAGE + (c / 8) * kPanel;
+            if (seen & (1u << i)) {
+                if (!warp_wait(&aux->q_empty[i], (phases >> i) & 1, aux, p.ctl)) return;
+                phases ^= 1u << i;
+            }
+            seen |= 1u << i;
+            const uint32_t tile = base + i * C::QTILE + (c / 8) * kQPanel;
             for (uint32_t r0 = warp * BATCH * QR; r0 < 128; r0 += kQueryWarps * BATCH * QR) {
                 // a lane finds one row; rows behind the last are zeros
                 const uint32_t mine = i * 128 + r0 + lane % (BATCH * QR);
@@ -374,26 +386,26 @@ __device__ __forceinline__ void query_role(const AttnParams &p, Work w, uint32_t
                 uint64_t o[BATCH];
 #pragma unroll
                 for (uint32_t u = 0; u < BATCH; ++u) o[u] = __shfl_sync(0xffffffffu, at, int(u * QR + lane / QL));
-                if constexpr (DT == SZ_BF16) {
-                    if (c * 8 < d) {
-#pragma unroll
-                        for (uint32_t u = 0; u < BATCH; ++u) {
-                            const uint32_t r = r0 + u * QR + lane / QL;
-                            const bool in = o[u] != kBadOffset;
-                            cp_async16(tile + r * 128 + (((c % 8) ^ (r & 7)) << 4), in ? q + o[u] + c * 16 : p.q.p, in);
-                        }
-                    }
-                } else {
-                    uint4 v[BATCH];
-#pragma unroll
-                    for (uint32_t u = 0; u < BATCH; ++u) {
-                        v[u] = make_uint4(0, 0, 0, 0);
-                        if (o[u] != kBadOffset && c * 8 < d) v[u] = *reinterpret_cast<const uint4 *>(q + o[u] + c * 16);
-                    }
+                if (c * 8 < d) {
 #pragma unroll
                     for (uint32_t u = 0; u < BATCH; ++u) {
                         const uint32_t r = r0 + u * QR + lane / QL;
-                        uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                        const bool in = o[u] != kBadOffset;
+                        cp_async16(tile + r * 128 + (((c % 8) ^ (r & 7)) << 4), in ? q + o[u] + c * 16 : p.q.p, in);
+                    }
+                }
+            }
+            cp_commit();
+            cp_wait<0>();
+            if constexpr (DT == SZ_FP8_E5M2) {
+                // to fp16, behind the row's power of two, each lane what it copied
+                for (uint32_t r0 = warp * BATCH * QR; r0 < 128; r0 += kQueryWarps * BATCH * QR) {
+#pragma unroll
+                    for (uint32_t u = 0; u < BATCH; ++u) {
+                        const uint32_t r = r0 + u * QR + lane / QL;
+                        const uint32_t at = tile + r * 128 + (((c % 8) ^ (r & 7)) << 4);
+                        const uint4 v = c * 8 < d ? lds_u128(at) : make_uint4(0, 0, 0, 0);
+                        uint32_t x[4] = {v.x, v.y, v.z, v.w};
                         float top = 0.f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
@@ -404,14 +416,11 @@ __device__ __forceinline__ void query_role(const AttnParams &p, Work w, uint32_t
                         const float up = __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) x[j] = pack_f16(bf16_lo(x[j]) * up, bf16_hi(x[j]) * up);
-                        if (c * 8 < d)
-                            sts_u128(tile + r * 128 + (((c % 8) ^ (r & 7)) << 4), make_uint4(x[0], x[1], x[2], x[3]));
+                        if (c * 8 < d) sts_u128(at, make_uint4(x[0], x[1], x[2], x[3]));
                         if (c == 0) aux->exp[i * 128 + r] = int8_t(e);
                     }
                 }
             }
-            cp_commit();
-            cp_wait<0>();
             fence_proxy_async_smem();
             bar_arrive(&aux->q_full[i]);
             __syncwarp();
@@ -429,7 +438,14 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
     const uint32_t d = p.cache.head_dim, ksteps = d / 16;
     const uint32_t qk_desc = instr_desc(DT, kTcBlock, false), pv_desc = instr_desc(DT, d, true);
     const bool leader = elect_one();
-    uint32_t kv = 0, p_uses[2] = {0, 0}, q_uses[2] = {0, 0};
+    uint32_t kv = 0;  // the part's first stage
+    uint32_t phases = 0;  // bit i: of q_full[i]; bit 2 + 2 i + b: of p_full[i][b]
+    auto wait = [&](uint64_t *bar, uint32_t bit) {
+        const bool ok = warp_wait(bar, (phases >> bit) & 1, aux, p.ctl);
+        phases ^= 1u << bit;
+        tc_after();
+        return ok;
+    };
     auto full = [&](uint32_t n) {
         const bool ok = warp_wait(&aux->full[n % C::STAGES], (n / C::STAGES) & 1, aux, p.ctl);
         tc_after();
@@ -441,76 +457,59 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
         __syncwarp();
     };
     auto release = [&](uint32_t n) { commit(&aux->empty[n % C::STAGES]); };
-    auto qk = [&](uint32_t i, uint32_t n) {
-        const uint64_t a = smem_desc(base + i * C::STAGE), b = stage(n);
+    auto qk = [&](uint32_t i, uint32_t b, uint32_t n) {
+        const uint64_t qd = smem_desc(base + i * C::QTILE), kd = stage(n);
         if (leader) {
 #pragma unroll
-            for (uint32_t k = 0; k < DP / 16; ++k) {
-                const uint64_t o = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
-                if (k < ksteps) mma_ss(tmem + i * 128, a + o, b + o, qk_desc, k > 0);
-            }
-            tc_commit(&aux->s_full[i]);
+            for (uint32_t k = 0; k < DP / 16; ++k)
+                if (k < ksteps)
+                    mma_ss(tmem + i * 128 + b * 64, qd + (((k / 4) * kQPanel + (k % 4) * 32) >> 4),
+                           kd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), qk_desc, k > 0);
+            tc_commit(&aux->s_full[i][b]);
         }
         __syncwarp();
     };
-    auto pv = [&](uint32_t i, uint32_t n, bool add) {
-        if (!warp_wait(&aux->p_full[i], p_uses[i]++ & 1, aux, p.ctl)) return false;
-        tc_after();
-        const uint64_t b = stage(n);
+    auto pv = [&](uint32_t i, uint32_t b, uint32_t n, bool add, bool last) {
+        const uint64_t vd = stage(n);
         if (leader) {
 #pragma unroll
             for (uint32_t k = 0; k < kTcBlock / 16; ++k)
-                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, b + k * (2048 >> 4), pv_desc, add || k > 0);
+                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + b * 64 + k * 8, vd + k * (2048 >> 4), pv_desc, add || k > 0);
+            tc_commit(&aux->o_done[i]);
+            if (last) tc_commit(&aux->o_last[i]);
         }
         __syncwarp();
-        return true;
-    };
-    auto queries = [&](uint32_t i) {
-        const bool ok = warp_wait(&aux->q_full[i], q_uses[i]++ & 1, aux, p.ctl);
-        tc_after();
-        return ok;
     };
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
-        const uint32_t n = t.to - t.from;
-        const bool two = t.rows > 128;
-        if (!full(kv)) return;
-        if (!queries(0)) return;
-        qk(0, kv);
-        if (n == 1) commit(&aux->q_empty[0]);
-        if (two) {
-            if (!queries(1)) return;
-            qk(1, kv);
-            if (n == 1) commit(&aux->q_empty[1]);
+        const uint32_t n = t.to - t.from, tiles = t.rows > 128 ? 2 : 1;
+        // stages of the part: k0, k1, v0, k2, v1, ..., v(n-2), v(n-1)
+        for (uint32_t j = 0; j < min(n, 2u); ++j) {
+            if (!full(kv + j)) return;
+            for (uint32_t i = 0; i < tiles; ++i) {
+                if (j == 0 && !wait(&aux->q_full[i], i)) return;
+                qk(i, j, kv + j);
+                if (j + 1 == n) commit(&aux->q_empty[i]);
+            }
+            release(kv + j);
         }
-        release(kv);
         for (uint32_t j = 0; j < n; ++j) {
-            const uint32_t v = kv + 1, k = kv + 2;
-            const bool more = j + 1 < n;
+            const uint32_t b = j & 1, v = kv + (j + 1 < n ? 2 * j + 2 : 2 * n - 1), k = kv + 2 * j + 3;
+            const bool more = j + 2 < n;
             if (!full(v)) return;
-            if (!pv(0, v, j > 0)) return;
-            if (more) {
-                if (!full(k)) return;
-                qk(0, k);
-                if (j + 2 == n) commit(&aux->q_empty[0]);
-            } else {
-                commit(&aux->o_full[0]);
-            }
-            if (two) {
-                if (!pv(1, v, j > 0)) return;
-                release(v);
+            for (uint32_t i = 0; i < tiles; ++i) {
+                if (!wait(&aux->p_full[i][b], 2 + 2 * i + b)) return;
+                pv(i, b, v, j > 0, j + 1 == n);
+                if (i + 1 == tiles) release(v);
                 if (more) {
-                    qk(1, k);
-                    if (j + 2 == n) commit(&aux->q_empty[1]);
-                } else {
-                    commit(&aux->o_full[1]);
+                    if (i == 0 && !full(k)) return;
+                    qk(i, b, k);
+                    if (j + 3 == n) commit(&aux->q_empty[i]);
+                    if (i + 1 == tiles) release(k);
                 }
-            } else {
-                release(v);
             }
-            if (more) release(k);
-            kv += 2;
         }
+        kv += 2 * n;
         if (!work_next<kTcRows>(p, w, t)) return;
     }
 }
@@ -523,7 +522,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
     const uint32_t lanes = (threadIdx.x & 96) << 16;  // the warp's quarter of tensor memory
     const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * 128;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    uint32_t q_uses = 0, s_uses = 0, o_uses = 0;
+    uint32_t q_uses = 0, s_phases = 0, o_uses = 0, o_parts = 0;
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const bool whole_tile = t.c_first == t.c_last;
@@ -546,27 +545,29 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
             __syncwarp();
             float m = -INFINITY, l = 0.f;
             for (uint32_t j = t.from; j < t.to; ++j) {
-                if (!warp_wait(&aux->s_full[i], s_uses++ & 1, aux, p.ctl)) return;
+                const uint32_t buf = (j - t.from) & 1;
+                if (!warp_wait(&aux->s_full[i][buf], (s_phases >> buf) & 1, aux, p.ctl)) return;
+                s_phases ^= 1u << buf;
                 tc_after();
-                uint32_t x[128];
-                tc_ld32(x, s_at);
-                tc_ld32(x + 32, s_at + 32);
-                tc_ld32(x + 64, s_at + 64);
-                tc_ld32(x + 96, s_at + 96);
+                uint32_t x[64];
+                tc_ld32(x, s_at + buf * 64);
+                tc_ld32(x + 32, s_at + buf * 64 + 32);
                 tc_wait_ld();
                 const uint32_t at = (t.block0 + j) * kTcBlock;
                 if (at < full_lo || at + kTcBlock > full_hi) {
                     // columns [a, b) of the block are seen
-                    const uint32_t a = rr.lo > at ? rr.lo - at : 0, b = rr.hi > at ? rr.hi - at : 0;
+                    const uint32_t a = min(rr.lo > at ? rr.lo - at : 0, 64u), b = min(rr.hi > at ? rr.hi - at : 0, 64u);
+                    const uint64_t seen = (b < 64 ? (1ull << b) - 1 : ~0ull) & (a < 64 ? ~0ull << a : 0ull);
+                    const uint32_t half[2] = {uint32_t(seen), uint32_t(seen >> 32)};
 #pragma unroll
-                    for (uint32_t c = 0; c < 128; ++c)
-                        if (c < a || c >= b) x[c] = 0xff800000u;
+                    for (uint32_t c = 0; c < 64; ++c)
+                        if (!(half[c / 32] & (1u << (c % 32)))) x[c] = 0xff800000u;
                 }
                 float tops[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tops[c] = __uint_as_float(x[c]);
 #pragma unroll
-                for (int c = 4; c < 128; ++c) tops[c & 3] = fmaxf(tops[c & 3], __uint_as_float(x[c]));
+                for (int c = 4; c < 64; ++c) tops[c & 3] = fmaxf(tops[c & 3], __uint_as_float(x[c]));
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * sc;
                 const bool grows = top > m + C::SLACK;
                 if (__any_sync(0xffffffffu, grows)) {
@@ -574,6 +575,9 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                     if (grows) m = top;
                     l *= c;
                     if (j > t.from) {
+                        // these scores are behind the product before the last one; the last may be under way
+                        if (!warp_wait(&aux->o_done[i], (o_uses - 1) & 1, aux, p.ctl)) return;
+                        tc_after();
                         for (uint32_t k = 0; k < d; k += 16) {
                             uint32_t o[16];
                             tc_ld16(o, o_at + k);
@@ -588,7 +592,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                 const uint64_t sc2 = f2(sc, sc), shift2 = f2(shift, shift);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < 64; c += 32) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -599,16 +603,17 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                         sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2(a, b));
                         pk[e / 2] = DT == SZ_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
                     }
-                    tc_st16(s_at + c / 2, pk);
+                    tc_st16(s_at + buf * 64 + c / 2, pk);
                 }
                 tc_wait_st();
                 tc_before();
-                bar_arrive(&aux->p_full[i]);
+                bar_arrive(&aux->p_full[i][buf]);
+                ++o_uses;
                 float a, b;
                 f2_split(f2_add(sum[0], sum[1]), a, b);
                 l += a + b;
             }
-            if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p.ctl)) return;
+            if (!warp_wait(&aux->o_last[i], o_parts++ & 1, aux, p.ctl)) return;
             tc_after();
             if (whole_tile) {
                 const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
@@ -638,14 +643,17 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                     if (worst != 0.f) aux->bad = 1;
                 }
             } else {
-                // columns of 256 rows, then the rows' m and l
+                // four columns of 256 rows at a time, then the rows' m and l
                 float *part = p.part + uint64_t(part_slot(blockIdx.x, t)) * kTcRows * (d + 2) + r;
+                float4 *quad = reinterpret_cast<float4 *>(part - r) + r;
                 for (uint32_t k = 0; k < d; k += 16) {
                     uint32_t o[16];
                     tc_ld16(o, o_at + k);
                     tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) part[(k + e) * kTcRows] = __uint_as_float(o[e]);
+                    for (int e = 0; e < 4; ++e)
+                        quad[(k / 4 + e) * kTcRows] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                                  __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                 }
                 part[d * kTcRows] = m;
                 part[(d + 1) * kTcRows] = l;
@@ -675,9 +683,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(&aux->q_full[i], 32 * kQueryWarps);
             mbar_init(&aux->q_empty[i], 1 + 4);  // the products, and the warps of the tile's softmax
-            mbar_init(&aux->s_full[i], 1);
-            mbar_init(&aux->p_full[i], 128);
-            mbar_init(&aux->o_full[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&aux->s_full[i][b], 1);
+                mbar_init(&aux->p_full[i][b], 128);
+            }
+            mbar_init(&aux->o_done[i], 1);
+            mbar_init(&aux->o_last[i], 1);
         }
         mbar_init(&aux->drain, 1);
         fence_mbar_init();
@@ -788,10 +799,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             for (uint32_t e = 0; e < COLS; ++e) v[e] = 0.f;
             for (uint32_t k = kg; k < parts; k += kJoinGroups) {
                 const float f = exp2_fast(__ldcg(slot(k) + d * kTcRows) - safe);
-                const float *from = slot(k) + col0 * kTcRows;
+                const float4 *from = reinterpret_cast<const float4 *>(slot(k) - r) + col0 / 4 * kTcRows + r;
 #pragma unroll
-                for (uint32_t e = 0; e < COLS; ++e)
-                    if (e < d / kJoinSplit) v[e] = fmaf(f, __ldcg(from + e * kTcRows), v[e]);
+                for (uint32_t e = 0; e < COLS; e += 4)
+                    if (e < d / kJoinSplit) {
+                        const float4 x = __ldcg(from + e / 4 * kTcRows);
+                        v[e] = fmaf(f, x.x, v[e]), v[e + 1] = fmaf(f, x.y, v[e + 1]);
+                        v[e + 2] = fmaf(f, x.z, v[e + 2]), v[e + 3] = fmaf(f, x.w, v[e + 3]);
+                    }
             }
             if (kg > 0) {
 #pragma unroll
