@@ -23,14 +23,22 @@
 // ex2 (16 a clock) and 2560 of matrix products (q k' of 64 columns reads 6 KB
 // of shared memory in what would be 32 clocks, and takes 48).
 //
-// The cache's pages are of any size and lie anywhere, so rows are fetched one by
-// one, by 16-byte asynchronous copies into the swizzled layout that the products
-// read.  An E5M2 cache's rows are copied as they are and spread to fp16 (E5M2 is
-// fp16's upper byte) on their way to that layout; queries are then fp16 too,
-// behind a power of two for each row that brings the row's largest below 2^14.
+// Keys and values come by tensor copies of 8 to 64 rows of a page, where pages
+// are a multiple of 8 tokens and all of the block is seen.  Other blocks, the
+// ends of what is seen among them, are fetched row by row by 16-byte
+// asynchronous copies, with zeros for places that nobody sees.  Both bring the
+// swizzled layout that the products read.  Row by row alone, a 2048-token chunk
+// over 8192 places took 306 us: the copies' issue, 20 clocks for 512 bytes, was
+// the bound.
+//
+// An E5M2 cache's rows come as they are and are spread to fp16 (E5M2 is fp16's
+// upper byte) on their way to that layout; queries are then fp16 too, behind a
+// power of two for each row that brings the row's largest below 2^14.
 //
 // A second kernel, which starts as the first one ends, joins the tiles that
 // several CTAs share, spread over all SMs.
+#include <cuda.h>
+
 #include "sz_attn.cuh"
 
 namespace sz {
@@ -70,6 +78,7 @@ struct TcCfg {
 
 struct TcAux {
     uint64_t full[10], empty[10];
+    uint64_t raw_full[8], raw_empty[8];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2][2], p_full[2][2];  // of a tile's buffers
     uint64_t o_done[2], o_last[2];        // a tile's product with values is done; its last of the part
@@ -116,6 +125,15 @@ __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+// One box of a tensor copy: elements x.., a head, rows from `token` of a page.
+__device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap *map, uint32_t x, uint32_t head, uint32_t token,
+                                           uint32_t page, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(head), "r"(token), "r"(page), "r"(smem_u32(bar))
+        : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -216,9 +234,25 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 // ------------------------------------------------------------------- roles
 
 // Keys and values into shared memory (warps 8-11), in the order in which they
-// are used: k0, k1, v0, k2, v1, ...
+// are used: k0, k1, v0, k2, v1, ...  `box`: rows of a tensor copy, 0 for none.
+struct Maps {
+    const CUtensorMap *k, *v;
+    uint32_t box;
+};
+
+// E5M2: 16 values of a row of the block to fp16, in the layout of the products.
+__device__ __forceinline__ void spread16(uint32_t block, uint32_t row, uint32_t piece, uint4 v) {
+    const uint4 lo = make_uint4(prmt(v.x, 0, 0x1404), prmt(v.x, 0, 0x3424), prmt(v.y, 0, 0x1404), prmt(v.y, 0, 0x3424));
+    const uint4 hi = make_uint4(prmt(v.z, 0, 0x1404), prmt(v.z, 0, 0x3424), prmt(v.w, 0, 0x1404), prmt(v.w, 0, 0x3424));
+    const uint32_t a = block + (piece / 4) * kPanel + row * 128, ch = 2 * (piece % 4);
+    // the lanes of the second panel go the other way round, off the first one's banks
+    const bool odd = piece >= 4;
+    sts_u128(a + (((ch + (odd ? 1 : 0)) ^ (row & 7)) << 4), odd ? hi : lo);
+    sts_u128(a + (((ch + (odd ? 0 : 1)) ^ (row & 7)) << 4), odd ? lo : hi);
+}
+
 template <int DT, int DP>
-__device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux) {
+__device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps, Work w, uint32_t base, TcAux *aux) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t LPR = DP * C::EB / 16;  // lanes to a row of the cache
     constexpr uint32_t ROWS = 32 / LPR;        // rows to an instruction
@@ -227,6 +261,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
     const uint32_t d = p.cache.head_dim;
     const uint32_t piece = lane % LPR, row0 = warp * 16 + lane / LPR;
     const bool has_piece = piece * 16 < d * C::EB;
+    uint32_t raws = 0;               // tiles that have gone through the raw ring
     uint32_t issued = 0, ready = 0;  // what is behind `ready` has been handed over
     auto hand_over = [&](uint32_t to) {
         if (ready == to) return;
@@ -240,6 +275,11 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
     };
     auto wait_free = [&](uint32_t n) {
         return n < C::STAGES || warp_wait(&aux->empty[n % C::STAGES], (n / C::STAGES - 1) & 1, aux, p.ctl);
+    };
+    // before giving up: the tensor copies that are under way land, or a limit passes
+    auto land = [&](uint64_t *bars, uint32_t ring, uint32_t n) {
+        for (uint32_t x = n > ring ? n - ring : 0; x < n; ++x)
+            for (uint32_t i = 0; i < 1u << 16 && !mbar_try_wait(&bars[x % ring], (x / ring) & 1); ++i) {}
     };
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
@@ -279,6 +319,105 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
             cp_commit();
         };
         const uint32_t blocks = t.to - t.from, tiles = 2 * blocks;
+        if (maps.box > 0) {
+            // A lane's box of a block: its page's id, or -1 if any of the boxes' ids is
+            // outside the pool or not all of the block is seen.
+            constexpr uint32_t PARTS = DT == SZ_BF16 ? C::PANELS : 1;  // boxes to a row: one for each panel, or raw rows
+            const uint32_t boxes = kTcBlock / maps.box * PARTS, mine = lane < boxes ? lane / PARTS : 0;
+            auto box_place = [&](uint32_t j) { return (t.block0 + j) * kTcBlock + mine * maps.box; };
+            auto box_id = [&](uint32_t j) -> int32_t {
+                const uint32_t at = (t.block0 + j) * kTcBlock;
+                if (j >= t.to || at < t.r.lo || at + kTcBlock > part_hi) return -1;
+                return __ldg(ids + div_by(box_place(j), p.cache.page_tokens));
+            };
+            // both kinds of a tile end in 128 arrivals at `bar`
+            auto fetch = [&](bool key, uint32_t j, int32_t id, uint32_t dst, uint32_t bytes, uint64_t *bar) {
+                if (__all_sync(0xffffffffu, id >= 0 && uint64_t(uint32_t(id)) < p.cache.pool_pages)) {
+                    if (tid == 0) mbar_arrive_expect_tx(bar, bytes);
+                    else bar_arrive(bar);
+                    __syncwarp();
+                    if (warp == 0 && lane < boxes) {
+                        const uint32_t at = box_place(j), panel = lane % PARTS;
+                        const uint32_t token = at - div_by(at, p.cache.page_tokens) * p.cache.page_tokens.d;
+                        const CUtensorMap *map = key ? maps.k : maps.v;
+                        if constexpr (DT == SZ_BF16)
+                            tensor_g2s(dst + panel * kPanel + mine * maps.box * 128, map, panel * 64, w.head, token, uint32_t(id), bar);
+                        else
+                            tensor_g2s(dst + mine * maps.box * DP, map, 0, w.head, token, uint32_t(id), bar);
+                    }
+                    __syncwarp();
+                    return;
+                }
+                const uint64_t off = offset(j, page_id(j));
+                copy(key ? p.cache.k : p.cache.v, off, [&](uint32_t u) {
+                    const uint32_t row = row0 + u * ROWS;
+                    return DT == SZ_BF16 ? dst + (piece / 8) * kPanel + row * 128 + (((piece % 8) ^ (row & 7)) << 4)
+                                         : dst + row * DP + piece * 16;
+                });
+                cp_wait<0>();
+                fence_proxy_async_smem();
+                bar_arrive(bar);
+                __syncwarp();
+            };
+            int32_t k_id = box_id(t.from), v_id[2] = {-1, -1};
+            uint32_t k_next = 0, v_next = 0;
+            auto next_fetch = [&](uint32_t n, uint32_t dst, uint32_t bytes, uint64_t *bar) {
+                if (n == 0 || ((n & 1) && k_next < blocks)) {
+                    const int32_t id = k_id;
+                    if (n == 0) v_id[0] = id;
+                    else v_id[1] = id;
+                    ++k_next;
+                    k_id = box_id(t.from + k_next);  // under way while this one is fetched
+                    fetch(true, t.from + k_next - 1, id, dst, bytes, bar);
+                } else {
+                    fetch(false, t.from + v_next++, v_id[0], dst, bytes, bar);
+                    v_id[0] = v_id[1];
+                }
+            };
+            if constexpr (DT == SZ_BF16) {
+                for (uint32_t n = 0; n < tiles; ++n, ++issued) {
+                    if (!wait_free(issued)) {
+                        land(aux->full, C::STAGES, issued);
+                        return;
+                    }
+                    next_fetch(n, base + C::RING_AT + (issued % C::STAGES) * C::STAGE, C::STAGE,
+                               &aux->full[issued % C::STAGES]);
+                }
+                ready = issued;
+            } else {
+                for (uint32_t n = 0; n < tiles + C::RAWS - 1; ++n) {
+                    if (n < tiles) {
+                        const uint32_t x = raws + n, slot = x % C::RAWS;
+                        if (x >= C::RAWS && !warp_wait(&aux->raw_empty[slot], (x / C::RAWS - 1) & 1, aux, p.ctl)) {
+                            land(aux->raw_full, C::RAWS, raws + n);
+                            return;
+                        }
+                        next_fetch(n, base + C::RAW_AT + slot * C::RAW, C::RAW, &aux->raw_full[slot]);
+                    }
+                    if (n + 1 < C::RAWS || n + 1 - C::RAWS >= tiles) continue;
+                    const uint32_t x = raws + n + 1 - C::RAWS, slot = x % C::RAWS;
+                    if (!warp_wait(&aux->raw_full[slot], (x / C::RAWS) & 1, aux, p.ctl) || !wait_free(issued)) {
+                        land(aux->raw_full, C::RAWS, raws + min(n + 1, tiles));
+                        return;
+                    }
+                    if (has_piece) {
+                        uint4 v[N];
+#pragma unroll
+                        for (uint32_t u = 0; u < N; ++u)
+                            v[u] = lds_u128(base + C::RAW_AT + slot * C::RAW + (row0 + u * ROWS) * DP + piece * 16);
+#pragma unroll
+                        for (uint32_t u = 0; u < N; ++u)
+                            spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + u * ROWS, piece, v[u]);
+                    }
+                    bar_arrive(&aux->raw_empty[slot]);
+                    ++issued;
+                    hand_over(issued);
+                }
+                raws += tiles;
+            }
+            if (!work_next<kTcRows>(p, w, t)) return;
+            continue;
+        }
         int32_t id = page_id(t.from);
         uint64_t k_off = offset(t.from, id), v_off[2] = {0, 0};  // of the next keys' block, and of the next values' two
         id = page_id(t.from + 1);
@@ -328,23 +467,13 @@ __device__ __forceinline__ void load_role(const AttnParams &p, Work w, uint32_t 
                 if (m >= tiles) continue;
                 cp_wait<C::RAWS - 1>();
                 if (!wait_free(issued)) return;
-                const uint32_t dst = base + C::RING_AT + (issued % C::STAGES) * C::STAGE + (piece / 4) * kPanel;
                 if (has_piece) {
                     uint4 v[N];
 #pragma unroll
                     for (uint32_t u = 0; u < N; ++u) v[u] = lds_u128(raw + (m % C::RAWS) * C::RAW + u * 2048);
 #pragma unroll
-                    for (uint32_t u = 0; u < N; ++u) {
-                        const uint4 lo = make_uint4(prmt(v[u].x, 0, 0x1404), prmt(v[u].x, 0, 0x3424),
-                                                    prmt(v[u].y, 0, 0x1404), prmt(v[u].y, 0, 0x3424));
-                        const uint4 hi = make_uint4(prmt(v[u].z, 0, 0x1404), prmt(v[u].z, 0, 0x3424),
-                                                    prmt(v[u].w, 0, 0x1404), prmt(v[u].w, 0, 0x3424));
-                        const uint32_t row = row0 + u * ROWS, a = dst + row * 128, ch = 2 * (piece % 4);
-                        // the lanes of the second panel go the other way round, off the first one's banks
-                        const bool odd = piece >= 4;
-                        sts_u128(a + (((ch + (odd ? 1 : 0)) ^ (row & 7)) << 4), odd ? hi : lo);
-                        sts_u128(a + (((ch + (odd ? 0 : 1)) ^ (row & 7)) << 4), odd ? lo : hi);
-                    }
+                    for (uint32_t u = 0; u < N; ++u)
+                        spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + u * ROWS, piece, v[u]);
                 }
                 ++issued;
                 hand_over(issued);
@@ -666,7 +795,9 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
 }
 
 template <int DT, int DP>
-__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map, uint32_t box) {
     using C = TcCfg<DT, DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -679,6 +810,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (uint32_t i = 0; i < C::STAGES; ++i) {
             mbar_init(&aux->full[i], 128);
             mbar_init(&aux->empty[i], 1);
+        }
+        for (int i = 0; i < int(C::RAWS); ++i) {
+            mbar_init(&aux->raw_full[i], 128);
+            mbar_init(&aux->raw_empty[i], 128);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&aux->q_full[i], 32 * kQueryWarps);
@@ -725,7 +860,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " SZ_TC_REGS_OTHER ";");
         if (warp < 12) {
-            load_role<DT, DP>(p, w, base, aux);
+            load_role<DT, DP>(p, Maps{&k_map, &v_map, box}, w, base, aux);
             cp_wait<0>();
         } else if (warp == 12) {
             mma_role<DT, DP>(p, w, base, aux, tmem);
@@ -869,13 +1004,52 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     }
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static std::atomic<void *> cache{nullptr};
+    void *f = cache.load(std::memory_order_acquire);
+    if (f) return reinterpret_cast<EncodeTiled>(f);
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+        return nullptr;
+    cache.store(f, std::memory_order_release);
+    return reinterpret_cast<EncodeTiled>(f);
+}
+
+// Pool as [pages, page_tokens, kv_heads, head_dim]; boxes of `box` rows of one
+// head: 64 elements in the products' swizzle, or whole E5M2 rows as they are.
+template <int DT, int DP>
+bool pool_map(CUtensorMap *map, const AttnParams &p, uint8_t *pool, uint32_t box) {
+    const CacheRef &c = p.cache;
+    const EncodeTiled encode = encode_tiled();
+    if (!encode || c.pool_pages >= (1ull << 31) || c.page_bytes >= (1ull << 40)) return false;
+    constexpr uint64_t EB = TcCfg<DT, DP>::EB;
+    const cuuint64_t dims[4] = {c.head_dim, c.kv_heads, c.page_tokens.d, c.pool_pages};
+    const cuuint64_t strides[3] = {c.head_dim * EB, c.row_bytes, c.page_bytes};
+    const cuuint32_t boxes[4] = {DT == SZ_BF16 ? 64u : uint32_t(DP), 1, box, 1}, one[4] = {1, 1, 1, 1};
+    return encode(map, DT == SZ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pool, dims,
+                  strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  DT == SZ_BF16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DT, int DP>
 sz_status run(const AttnParams &p, int num_sms, cudaStream_t stream) {
     using C = TcCfg<DT, DP>;
     static std::atomic<int> cache[kMaxDevices];
     auto kern = attn_tc_kernel<DT, DP>;
     if (resident_per_sm(reinterpret_cast<const void *>(kern), kTcThreads, C::SMEM, cache) <= 0) return SZ_ERR_CUDA;
-    if (launch_pdl(kern, unsigned(num_sms), kTcThreads, C::SMEM, stream, p) != cudaSuccess) return SZ_ERR_CUDA;
+    // rows of a box: the largest power of two that divides a page, from 8 (a swizzle atom) to a block
+    CUtensorMap k_map{}, v_map{};
+    uint32_t box = p.cache.page_tokens.d & (0u - p.cache.page_tokens.d);
+    box = box < 8 ? 0 : (box < uint32_t(kTcBlock) ? box : uint32_t(kTcBlock));
+    if (box && !(pool_map<DT, DP>(&k_map, p, p.cache.k, box) && pool_map<DT, DP>(&v_map, p, p.cache.v, box))) box = 0;
+    if (launch_pdl(kern, unsigned(num_sms), kTcThreads, C::SMEM, stream, p, k_map, v_map, box) != cudaSuccess)
+        return SZ_ERR_CUDA;
     return launch_pdl(attn_join_kernel<DT, DP>, unsigned(num_sms) * kJoinSlices, kJoinThreads, 0, stream, p) ==
                    cudaSuccess
                ? SZ_OK
