@@ -10,10 +10,12 @@
 //   warps 0-3, 4-7  softmax of the first and the second tile, a thread a row:
 //                   a row's maximum and sum need no exchange between threads
 //   warps 8-11      keys and values into shared memory
-//   warp 12         issues the products: for each block and tile p v, then q k'
+//   warps 12, 13    issue the products of a tile: for each block p v, then q k'
 //                   of the block after the next into the buffer that is free
-//                   now, so that a softmax finds its next scores ready
-//   warps 13-15     queries into shared memory: a tile's as soon as its last
+//                   now, so that a softmax finds its next scores ready (one
+//                   warp for both tiles took 1.6 us for a block's waits, issues
+//                   and announcements, three times the products' time)
+//   warps 14, 15    queries into shared memory: a tile's as soon as its last
 //                   product with the ones before is done
 // m is the largest score so far only to within 2^SLACK: the sums are rescaled
 // (through registers) when a row's maximum has grown by more, so that most
@@ -82,7 +84,7 @@ struct TcAux {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2][2], p_full[2][2];  // of a tile's buffers
     uint64_t o_done[2], o_last[2];        // a tile's product with values is done; its last of the part
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem, abort, bad;
     int8_t exp[kTcRows];  // E5M2: exponent taken out of each query row
 };
@@ -484,14 +486,14 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
     }
 }
 
-// Queries into shared memory (warps 13-15).
-constexpr uint32_t kQueryWarps = 3;
+// Queries into shared memory (warps 14, 15).
+constexpr uint32_t kQueryWarps = 2;
 template <int DT, int DP>
 __device__ __forceinline__ void query_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t QL = DP / 8, QR = 32 / QL;          // lanes to a row, rows to an instruction
     constexpr uint32_t BATCH = 8;
-    const uint32_t lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 13, c = lane % QL;
+    const uint32_t lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 14, c = lane % QL;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
     uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i]
     for (;;) {
@@ -558,17 +560,19 @@ __device__ __forceinline__ void query_role(const AttnParams &p, Work w, uint32_t
     }
 }
 
-// The products.  The warp goes through the loop together and one elected lane
-// issues: behind a test of the thread's own number the compiler does not see
-// that one lane is left, and each product took twice as long.
+// The products of tile i (warps 12 and 13).  A warp goes through the loop
+// together and one elected lane issues: behind a test of the thread's own number
+// the compiler does not see that one lane is left, and each product took twice
+// as long.  All of tensor memory is this CTA's, so its addresses are constants.
 template <int DT, int DP>
-__device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux, uint32_t tmem) {
+__device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux, uint32_t i) {
     using C = TcCfg<DT, DP>;
     const uint32_t d = p.cache.head_dim, ksteps = d / 16;
     const uint32_t qk_desc = instr_desc(DT, kTcBlock, false), pv_desc = instr_desc(DT, d, true);
     const bool leader = elect_one();
-    uint32_t kv = 0;  // the part's first stage
-    uint32_t phases = 0;  // bit i: of q_full[i]; bit 2 + 2 i + b: of p_full[i][b]
+    uint32_t kv = 0;      // the part's first stage
+    uint32_t phases = 0;  // bit 2: of q_full[i]; bit b: of p_full[i][b]
+    const uint64_t qd = smem_desc(base + i * C::QTILE);
     auto wait = [&](uint64_t *bar, uint32_t bit) {
         const bool ok = warp_wait(bar, (phases >> bit) & 1, aux, p.ctl);
         phases ^= 1u << bit;
@@ -581,61 +585,59 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
         return ok;
     };
     auto stage = [&](uint32_t n) { return smem_desc(base + C::RING_AT + (n % C::STAGES) * C::STAGE); };
-    auto commit = [&](uint64_t *bar) {
-        if (leader) tc_commit(bar);
-        __syncwarp();
-    };
-    auto release = [&](uint32_t n) { commit(&aux->empty[n % C::STAGES]); };
-    auto qk = [&](uint32_t i, uint32_t b, uint32_t n) {
-        const uint64_t qd = smem_desc(base + i * C::QTILE), kd = stage(n);
+    // scores of the block with keys in stage n; the stage is free behind them, the queries if they are the last
+    auto qk = [&](uint32_t b, uint32_t n, bool last) {
+        const uint64_t kd = stage(n);
         if (leader) {
 #pragma unroll
             for (uint32_t k = 0; k < DP / 16; ++k)
                 if (k < ksteps)
-                    mma_ss(tmem + i * 128 + b * 64, qd + (((k / 4) * kQPanel + (k % 4) * 32) >> 4),
+                    mma_ss(i * 128 + b * 64, qd + (((k / 4) * kQPanel + (k % 4) * 32) >> 4),
                            kd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), qk_desc, k > 0);
             tc_commit(&aux->s_full[i][b]);
+            tc_commit(&aux->empty[n % C::STAGES]);
+            if (last) tc_commit(&aux->q_empty[i]);
         }
         __syncwarp();
     };
-    auto pv = [&](uint32_t i, uint32_t b, uint32_t n, bool add, bool last) {
+    auto pv = [&](uint32_t b, uint32_t n, bool add, bool last) {
         const uint64_t vd = stage(n);
         if (leader) {
 #pragma unroll
             for (uint32_t k = 0; k < kTcBlock / 16; ++k)
-                mma_ts(tmem + 256 + i * 128, tmem + i * 128 + b * 64 + k * 8, vd + k * (2048 >> 4), pv_desc, add || k > 0);
+                mma_ts(256 + i * 128, i * 128 + b * 64 + k * 8, vd + k * (2048 >> 4), pv_desc, add || k > 0);
             tc_commit(&aux->o_done[i]);
+            tc_commit(&aux->empty[n % C::STAGES]);
             if (last) tc_commit(&aux->o_last[i]);
         }
         __syncwarp();
     };
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
-        const uint32_t n = t.to - t.from, tiles = t.rows > 128 ? 2 : 1;
-        // stages of the part: k0, k1, v0, k2, v1, ..., v(n-2), v(n-1)
-        for (uint32_t j = 0; j < min(n, 2u); ++j) {
-            if (!full(kv + j)) return;
-            for (uint32_t i = 0; i < tiles; ++i) {
-                if (j == 0 && !wait(&aux->q_full[i], i)) return;
-                qk(i, j, kv + j);
-                if (j + 1 == n) commit(&aux->q_empty[i]);
+        const uint32_t n = t.to - t.from;
+        if (i * 128 < t.rows) {
+            // stages of the part: k0, k1, v0, k2, v1, ..., v(n-2), v(n-1)
+            for (uint32_t j = 0; j < min(n, 2u); ++j) {
+                if (!full(kv + j)) return;
+                if (j == 0 && !wait(&aux->q_full[i], 2)) return;
+                qk(j, kv + j, j + 1 == n);
             }
-            release(kv + j);
-        }
-        for (uint32_t j = 0; j < n; ++j) {
-            const uint32_t b = j & 1, v = kv + (j + 1 < n ? 2 * j + 2 : 2 * n - 1), k = kv + 2 * j + 3;
-            const bool more = j + 2 < n;
-            if (!full(v)) return;
-            for (uint32_t i = 0; i < tiles; ++i) {
-                if (!wait(&aux->p_full[i][b], 2 + 2 * i + b)) return;
-                pv(i, b, v, j > 0, j + 1 == n);
-                if (i + 1 == tiles) release(v);
-                if (more) {
-                    if (i == 0 && !full(k)) return;
-                    qk(i, b, k);
-                    if (j + 3 == n) commit(&aux->q_empty[i]);
-                    if (i + 1 == tiles) release(k);
+            for (uint32_t j = 0; j < n; ++j) {
+                const uint32_t b = j & 1, v = kv + (j + 1 < n ? 2 * j + 2 : 2 * n - 1), k = kv + 2 * j + 3;
+                if (!full(v)) return;
+                if (!wait(&aux->p_full[i][b], b)) return;
+                pv(b, v, j > 0, j + 1 == n);
+                if (j + 2 < n) {
+                    if (!full(k)) return;
+                    qk(b, k, j + 3 == n);
                 }
+            }
+        } else {
+            // the other tile's stages need this one's word too
+            for (uint32_t j = 0; j < 2 * n; ++j) {
+                if (!full(kv + j)) return;
+                if (leader) bar_arrive(&aux->empty[(kv + j) % C::STAGES]);
+                __syncwarp();
             }
         }
         kv += 2 * n;
@@ -645,11 +647,11 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
 
 // Softmax of one tile's rows, a thread a row, and what becomes of the sums.
 template <int DT, int DP>
-__device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux *aux, uint32_t tmem, TcDesc *desc) {
+__device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux *aux, TcDesc *desc) {
     using C = TcCfg<DT, DP>;
     const uint32_t i = threadIdx.x / 128, row = threadIdx.x & 127;
     const uint32_t lanes = (threadIdx.x & 96) << 16;  // the warp's quarter of tensor memory
-    const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * 128;
+    const uint32_t s_at = lanes + i * 128, o_at = lanes + 256 + i * 128;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
     uint32_t q_uses = 0, s_phases = 0, o_uses = 0, o_parts = 0;
     for (;;) {
@@ -809,7 +811,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (tid == 0) {
         for (uint32_t i = 0; i < C::STAGES; ++i) {
             mbar_init(&aux->full[i], 128);
-            mbar_init(&aux->empty[i], 1);
+            mbar_init(&aux->empty[i], 2);
         }
         for (int i = 0; i < int(C::RAWS); ++i) {
             mbar_init(&aux->raw_full[i], 128);
@@ -825,7 +827,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&aux->o_done[i], 1);
             mbar_init(&aux->o_last[i], 1);
         }
-        mbar_init(&aux->drain, 1);
+        mbar_init(&aux->drain[0], 1);
+        mbar_init(&aux->drain[1], 1);
         fence_mbar_init();
         aux->abort = 0;
         aux->bad = 0;
@@ -856,19 +859,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 " SZ_TC_REGS_SOFTMAX ";");
-        softmax_role<DT, DP>(p, w, aux, tmem, desc);
+        softmax_role<DT, DP>(p, w, aux, desc);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " SZ_TC_REGS_OTHER ";");
         if (warp < 12) {
             load_role<DT, DP>(p, Maps{&k_map, &v_map, box}, w, base, aux);
             cp_wait<0>();
-        } else if (warp == 12) {
-            mma_role<DT, DP>(p, w, base, aux, tmem);
+        } else if (warp < 14) {
+            mma_role<DT, DP>(p, w, base, aux, warp - 12);
             // nothing of this CTA's is under way when it gives its memory back
             __syncwarp();
-            if (elect_one()) tc_commit(&aux->drain);
+            if (elect_one()) tc_commit(&aux->drain[warp - 12]);
             __syncwarp();
-            warp_wait(&aux->drain, 0, aux, p.ctl);
+            warp_wait(&aux->drain[warp - 12], 0, aux, p.ctl);
         } else {
             query_role<DT, DP>(p, w, base, aux);
             cp_wait<0>();
