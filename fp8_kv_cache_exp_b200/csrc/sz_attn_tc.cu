@@ -4,26 +4,26 @@
 //   x = scale * q . k,  p = exp(x - m),  o = sum p v / sum p
 //
 // A CTA takes 256 rows of one sequence and KV head, as two tiles of 128, and
-// goes over their places in blocks of 64.  Scores, p and the sums of p v stay
-// in tensor memory: per tile two buffers of 64 columns of scores, which p
-// overwrites in 16 bits, and 128 columns of sums.  The roles:
+// goes over their places in blocks of 128.  Scores, p and the sums of p v stay
+// in tensor memory: per tile 128 columns of scores, which p overwrites in 16
+// bits, and 128 columns of sums.  The roles:
 //   warps 0-3, 4-7  softmax of the first and the second tile, a thread a row:
 //                   a row's maximum and sum need no exchange between threads
 //   warps 8-11      keys and values into shared memory
-//   warps 12, 13    issue the products of a tile: for each block p v, then q k'
-//                   of the block after the next into the buffer that is free
-//                   now, so that a softmax finds its next scores ready (one
-//                   warp for both tiles took 1.6 us for a block's waits, issues
-//                   and announcements, three times the products' time)
+//   warps 12, 13    issue the products of a tile: p v, in two halves as p comes,
+//                   then q k' of the next block; the other tile's products run
+//                   while this one's softmax does
 //   warps 14, 15    queries into shared memory: a tile's as soon as its last
 //                   product with the ones before is done
 // m is the largest score so far only to within 2^SLACK: the sums are rescaled
 // (through registers) when a row's maximum has grown by more, so that most
 // blocks leave them where they are.
 //
-// What bounds it: 128 places of 256 rows and heads of 128 are 2048 clocks of
-// ex2 (16 a clock) and 2560 of matrix products (q k' of 64 columns reads 6 KB
-// of shared memory in what would be 32 clocks, and takes 48).
+// What bounds it: a block of 256 rows and heads of 128 is 2048 clocks of matrix
+// products and 2048 clocks of ex2 (16 a clock), if each tile's chain (scores,
+// softmax, products) takes no longer.  Blocks of 64 places with two buffers of
+// scores have shorter chains, but q k' of 64 columns reads 6 KB of shared memory
+// in what would be 32 clocks, and takes 48.
 //
 // Keys and values come by tensor copies of 8 to 64 rows of a page, where pages
 // are a multiple of 8 tokens and all of the block is seen.  Other blocks, the
@@ -50,13 +50,13 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;
-constexpr int kTcBlock = 64;
+constexpr int kTcBlock = 128;
 constexpr uint32_t kQPanel = 128 * 128;       // bytes of 128 rows of 64 16-bit elements
 constexpr uint32_t kPanel = kTcBlock * 128;   // of a block's rows
-// registers of a softmax thread and of the others: 256 * 152 + 256 * 104 = 512 * 128,
+// registers of a softmax thread and of the others: 256 * 192 + 256 * 64 = 512 * 128,
 // what the CTA is launched with
-#define SZ_TC_REGS_SOFTMAX "152"
-#define SZ_TC_REGS_OTHER "104"
+#define SZ_TC_REGS_SOFTMAX "192"
+#define SZ_TC_REGS_OTHER "64"
 
 template <int DT, int DP>
 struct TcCfg {
@@ -64,9 +64,9 @@ struct TcCfg {
     static constexpr uint32_t PANELS = DP / 64;
     static constexpr uint32_t QTILE = PANELS * kQPanel;
     static constexpr uint32_t STAGE = PANELS * kPanel;       // a block's keys or values
-    static constexpr uint32_t STAGES = DT == SZ_BF16 ? 10 : 6;
+    static constexpr uint32_t STAGES = (DT == SZ_BF16 ? 10 : 6) / PANELS;
     static constexpr uint32_t RAW = kTcBlock * DP;           // E5M2: as they come
-    static constexpr uint32_t RAWS = DT == SZ_BF16 ? 0 : 8;
+    static constexpr uint32_t RAWS = (DT == SZ_BF16 ? 0 : 8) / PANELS;
     static constexpr uint32_t RING_AT = 2 * QTILE;           // behind the queries
     static constexpr uint32_t RAW_AT = RING_AT + STAGES * STAGE;
     static constexpr uint32_t AUX_AT = RAW_AT + RAWS * RAW;
@@ -82,8 +82,8 @@ struct TcAux {
     uint64_t full[10], empty[10];
     uint64_t raw_full[8], raw_empty[8];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2][2], p_full[2][2];  // of a tile's buffers
-    uint64_t o_done[2], o_last[2];        // a tile's product with values is done; its last of the part
+    uint64_t s_full[2], p_full[2][2];  // a tile's scores; the halves of its weights
+    uint64_t o_full[2];                // a tile's sums, at the end of a part
     uint64_t drain[2];
     uint32_t tmem, abort, bad;
     int8_t exp[kTcRows];  // E5M2: exponent taken out of each query row
@@ -213,6 +213,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Two floats at a time.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
     uint64_t r;
@@ -236,7 +242,7 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 // ------------------------------------------------------------------- roles
 
 // Keys and values into shared memory (warps 8-11), in the order in which they
-// are used: k0, k1, v0, k2, v1, ...  `box`: rows of a tensor copy, 0 for none.
+// are used: k0, v0, k1, v1, ...  `box`: rows of a tensor copy, 0 for none.
 struct Maps {
     const CUtensorMap *k, *v;
     uint32_t box;
@@ -258,10 +264,10 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
     using C = TcCfg<DT, DP>;
     constexpr uint32_t LPR = DP * C::EB / 16;  // lanes to a row of the cache
     constexpr uint32_t ROWS = 32 / LPR;        // rows to an instruction
-    constexpr uint32_t N = 16 / ROWS;          // instructions to a warp's 16 rows of a block
+    constexpr uint32_t N = 32 / ROWS;          // instructions to a warp's 32 rows of a block
     const uint32_t tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
     const uint32_t d = p.cache.head_dim;
-    const uint32_t piece = lane % LPR, row0 = warp * 16 + lane / LPR;
+    const uint32_t piece = lane % LPR, row0 = warp * 32 + lane / LPR;
     const bool has_piece = piece * 16 < d * C::EB;
     uint32_t raws = 0;               // tiles that have gone through the raw ring
     uint32_t issued = 0, ready = 0;  // what is behind `ready` has been handed over
@@ -290,7 +296,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
         const uint64_t head_off = uint64_t(w.head) * d * C::EB + piece * 16;
 
         // the place of this lane's row of a block, and its page's id
-        auto place = [&](uint32_t j) { return (t.block0 + j) * kTcBlock + warp * 16 + (lane & 15); };
+        auto place = [&](uint32_t j) { return (t.block0 + j) * kTcBlock + warp * 32 + lane; };
         auto page_id = [&](uint32_t j) -> int32_t {
             const uint32_t at = place(j);
             return j < t.to && at >= t.r.lo && at < part_hi ? __ldg(ids + div_by(at, p.cache.page_tokens)) : 0;
@@ -305,17 +311,22 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
             }
             return uint64_t(id) * p.cache.page_bytes + uint64_t(at - page * p.cache.page_tokens.d) * p.cache.row_bytes;
         };
-        // Offsets of all of a lane's rows first: one by one, the shuffles' latency
+        // Offsets of eight of a lane's rows first: one by one, the shuffles' latency
         // bounds the copies.
         auto copy = [&](const uint8_t *pool, uint64_t off, auto &&to) {
-            uint64_t o[N];
+            constexpr uint32_t STEP = N < 8 ? N : 8;
 #pragma unroll
-            for (uint32_t u = 0; u < N; ++u) o[u] = __shfl_sync(0xffffffffu, off, int(u * ROWS + lane / LPR));
-            if (has_piece) {
+            for (uint32_t u0 = 0; u0 < N; u0 += STEP) {
+                uint64_t o[STEP];
 #pragma unroll
-                for (uint32_t u = 0; u < N; ++u) {
-                    const bool in = o[u] != kBadOffset;
-                    cp_async16(to(u), pool + (in ? o[u] + head_off : 0), in);
+                for (uint32_t u = 0; u < STEP; ++u)
+                    o[u] = __shfl_sync(0xffffffffu, off, int((u0 + u) * ROWS + lane / LPR));
+                if (has_piece) {
+#pragma unroll
+                    for (uint32_t u = 0; u < STEP; ++u) {
+                        const bool in = o[u] != kBadOffset;
+                        cp_async16(to(u0 + u), pool + (in ? o[u] + head_off : 0), in);
+                    }
                 }
             }
             cp_commit();
@@ -361,20 +372,14 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
                 bar_arrive(bar);
                 __syncwarp();
             };
-            int32_t k_id = box_id(t.from), v_id[2] = {-1, -1};
-            uint32_t k_next = 0, v_next = 0;
+            int32_t id = box_id(t.from), ahead = box_id(t.from + 1);
             auto next_fetch = [&](uint32_t n, uint32_t dst, uint32_t bytes, uint64_t *bar) {
-                if (n == 0 || ((n & 1) && k_next < blocks)) {
-                    const int32_t id = k_id;
-                    if (n == 0) v_id[0] = id;
-                    else v_id[1] = id;
-                    ++k_next;
-                    k_id = box_id(t.from + k_next);  // under way while this one is fetched
-                    fetch(true, t.from + k_next - 1, id, dst, bytes, bar);
-                } else {
-                    fetch(false, t.from + v_next++, v_id[0], dst, bytes, bar);
-                    v_id[0] = v_id[1];
+                const uint32_t j = t.from + n / 2;
+                if (n > 0 && (n & 1) == 0) {
+                    id = ahead;
+                    ahead = box_id(j + 1);  // under way while this block is fetched
                 }
+                fetch((n & 1) == 0, j, id, dst, bytes, bar);
             };
             if constexpr (DT == SZ_BF16) {
                 for (uint32_t n = 0; n < tiles; ++n, ++issued) {
@@ -403,13 +408,16 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
                         return;
                     }
                     if (has_piece) {
-                        uint4 v[N];
 #pragma unroll
-                        for (uint32_t u = 0; u < N; ++u)
-                            v[u] = lds_u128(base + C::RAW_AT + slot * C::RAW + (row0 + u * ROWS) * DP + piece * 16);
+                        for (uint32_t u0 = 0; u0 < N; u0 += 4) {
+                            uint4 v[4];
 #pragma unroll
-                        for (uint32_t u = 0; u < N; ++u)
-                            spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + u * ROWS, piece, v[u]);
+                            for (uint32_t u = 0; u < 4; ++u)
+                                v[u] = lds_u128(base + C::RAW_AT + slot * C::RAW + (row0 + (u0 + u) * ROWS) * DP + piece * 16);
+#pragma unroll
+                            for (uint32_t u = 0; u < 4; ++u)
+                                spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + (u0 + u) * ROWS, piece, v[u]);
+                        }
                     }
                     bar_arrive(&aux->raw_empty[slot]);
                     ++issued;
@@ -421,25 +429,13 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
             continue;
         }
         int32_t id = page_id(t.from);
-        uint64_t k_off = offset(t.from, id), v_off[2] = {0, 0};  // of the next keys' block, and of the next values' two
-        id = page_id(t.from + 1);
-        uint32_t k_next = 0;
-        // the next tile in order: keys if they are not a block ahead of the values
+        uint64_t off = 0;
         auto next_copy = [&](uint32_t n, auto &&to) {
-            const bool key = n == 0 || ((n & 1) && k_next < blocks);
-            if (key) {
-                copy(p.cache.k, k_off, to);
-                if (n == 0) v_off[0] = k_off;
-                else v_off[1] = k_off;
-                ++k_next;
-            } else {
-                copy(p.cache.v, v_off[0], to);
-                v_off[0] = v_off[1];
+            if ((n & 1) == 0) {
+                off = offset(t.from + n / 2, id);
+                id = page_id(t.from + n / 2 + 1);
             }
-            if (key && k_next < blocks) {
-                k_off = offset(t.from + k_next, id);
-                id = page_id(t.from + k_next + 1);
-            }
+            copy((n & 1) ? p.cache.v : p.cache.k, off, to);
         };
         if constexpr (DT == SZ_BF16) {
             for (uint32_t n = 0; n < tiles; ++n) {
@@ -454,8 +450,8 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
                     return dst + row * 128 + (((piece % 8) ^ (row & 7)) << 4);
                 });
                 ++issued;
-                cp_wait<4>();
-                if (issued > ready + 4) hand_over(issued - 4);
+                cp_wait<2>();
+                if (issued > ready + 2) hand_over(issued - 2);
             }
             cp_wait<0>();
             hand_over(issued);
@@ -470,12 +466,15 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
                 cp_wait<C::RAWS - 1>();
                 if (!wait_free(issued)) return;
                 if (has_piece) {
-                    uint4 v[N];
 #pragma unroll
-                    for (uint32_t u = 0; u < N; ++u) v[u] = lds_u128(raw + (m % C::RAWS) * C::RAW + u * 2048);
+                    for (uint32_t u0 = 0; u0 < N; u0 += 4) {
+                        uint4 v[4];
 #pragma unroll
-                    for (uint32_t u = 0; u < N; ++u)
-                        spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + u * ROWS, piece, v[u]);
+                        for (uint32_t u = 0; u < 4; ++u) v[u] = lds_u128(raw + (m % C::RAWS) * C::RAW + (u0 + u) * 2048);
+#pragma unroll
+                        for (uint32_t u = 0; u < 4; ++u)
+                            spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + (u0 + u) * ROWS, piece, v[u]);
+                    }
                 }
                 ++issued;
                 hand_over(issued);
@@ -571,7 +570,7 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
     const uint32_t qk_desc = instr_desc(DT, kTcBlock, false), pv_desc = instr_desc(DT, d, true);
     const bool leader = elect_one();
     uint32_t kv = 0;      // the part's first stage
-    uint32_t phases = 0;  // bit 2: of q_full[i]; bit b: of p_full[i][b]
+    uint32_t phases = 0;  // bit 2: of q_full[i]; bit h: of p_full[i][h]
     const uint64_t qd = smem_desc(base + i * C::QTILE);
     auto wait = [&](uint64_t *bar, uint32_t bit) {
         const bool ok = warp_wait(bar, (phases >> bit) & 1, aux, p.ctl);
@@ -586,29 +585,25 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
     };
     auto stage = [&](uint32_t n) { return smem_desc(base + C::RING_AT + (n % C::STAGES) * C::STAGE); };
     // scores of the block with keys in stage n; the stage is free behind them, the queries if they are the last
-    auto qk = [&](uint32_t b, uint32_t n, bool last) {
+    auto qk = [&](uint32_t n, bool last) {
         const uint64_t kd = stage(n);
         if (leader) {
 #pragma unroll
             for (uint32_t k = 0; k < DP / 16; ++k)
                 if (k < ksteps)
-                    mma_ss(i * 128 + b * 64, qd + (((k / 4) * kQPanel + (k % 4) * 32) >> 4),
+                    mma_ss(i * 128, qd + (((k / 4) * kQPanel + (k % 4) * 32) >> 4),
                            kd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), qk_desc, k > 0);
-            tc_commit(&aux->s_full[i][b]);
+            tc_commit(&aux->s_full[i]);
             tc_commit(&aux->empty[n % C::STAGES]);
             if (last) tc_commit(&aux->q_empty[i]);
         }
         __syncwarp();
     };
-    auto pv = [&](uint32_t b, uint32_t n, bool add, bool last) {
-        const uint64_t vd = stage(n);
+    auto pv = [&](uint32_t half, uint64_t vd, bool add) {
         if (leader) {
 #pragma unroll
-            for (uint32_t k = 0; k < kTcBlock / 16; ++k)
-                mma_ts(256 + i * 128, i * 128 + b * 64 + k * 8, vd + k * (2048 >> 4), pv_desc, add || k > 0);
-            tc_commit(&aux->o_done[i]);
-            tc_commit(&aux->empty[n % C::STAGES]);
-            if (last) tc_commit(&aux->o_last[i]);
+            for (uint32_t k = half * 4; k < half * 4 + 4; ++k)
+                mma_ts(256 + i * 128, i * 128 + k * 8, vd + k * (2048 >> 4), pv_desc, add || k > 0);
         }
         __syncwarp();
     };
@@ -616,20 +611,25 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const uint32_t n = t.to - t.from;
         if (i * 128 < t.rows) {
-            // stages of the part: k0, k1, v0, k2, v1, ..., v(n-2), v(n-1)
-            for (uint32_t j = 0; j < min(n, 2u); ++j) {
-                if (!full(kv + j)) return;
-                if (j == 0 && !wait(&aux->q_full[i], 2)) return;
-                qk(j, kv + j, j + 1 == n);
-            }
+            if (!full(kv)) return;
+            if (!wait(&aux->q_full[i], 2)) return;
+            qk(kv, n == 1);
             for (uint32_t j = 0; j < n; ++j) {
-                const uint32_t b = j & 1, v = kv + (j + 1 < n ? 2 * j + 2 : 2 * n - 1), k = kv + 2 * j + 3;
+                const uint32_t v = kv + 2 * j + 1, k = v + 1;
+                const uint64_t vd = stage(v);
                 if (!full(v)) return;
-                if (!wait(&aux->p_full[i][b], b)) return;
-                pv(b, v, j > 0, j + 1 == n);
-                if (j + 2 < n) {
+                if (!wait(&aux->p_full[i][0], 0)) return;
+                pv(0, vd, j > 0);
+                if (!wait(&aux->p_full[i][1], 1)) return;
+                pv(1, vd, true);
+                if (leader) {
+                    tc_commit(&aux->empty[v % C::STAGES]);
+                    if (j + 1 == n) tc_commit(&aux->o_full[i]);
+                }
+                __syncwarp();
+                if (j + 1 < n) {
                     if (!full(k)) return;
-                    qk(b, k, j + 3 == n);
+                    qk(k, j + 2 == n);
                 }
             }
         } else {
@@ -653,7 +653,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
     const uint32_t lanes = (threadIdx.x & 96) << 16;  // the warp's quarter of tensor memory
     const uint32_t s_at = lanes + i * 128, o_at = lanes + 256 + i * 128;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    uint32_t q_uses = 0, s_phases = 0, o_uses = 0, o_parts = 0;
+    uint32_t q_uses = 0, s_uses = 0, o_uses = 0;
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const bool whole_tile = t.c_first == t.c_last;
@@ -676,29 +676,38 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
             __syncwarp();
             float m = -INFINITY, l = 0.f;
             for (uint32_t j = t.from; j < t.to; ++j) {
-                const uint32_t buf = (j - t.from) & 1;
-                if (!warp_wait(&aux->s_full[i][buf], (s_phases >> buf) & 1, aux, p.ctl)) return;
-                s_phases ^= 1u << buf;
+                if (!warp_wait(&aux->s_full[i], s_uses++ & 1, aux, p.ctl)) return;
                 tc_after();
-                uint32_t x[64];
-                tc_ld32(x, s_at + buf * 64);
-                tc_ld32(x + 32, s_at + buf * 64 + 32);
+                uint32_t x[128];
+                tc_ld32(x, s_at);
+                tc_ld32(x + 32, s_at + 32);
+                tc_ld32(x + 64, s_at + 64);
+                tc_ld32(x + 96, s_at + 96);
                 tc_wait_ld();
                 const uint32_t at = (t.block0 + j) * kTcBlock;
                 if (at < full_lo || at + kTcBlock > full_hi) {
                     // columns [a, b) of the block are seen
-                    const uint32_t a = min(rr.lo > at ? rr.lo - at : 0, 64u), b = min(rr.hi > at ? rr.hi - at : 0, 64u);
-                    const uint64_t seen = (b < 64 ? (1ull << b) - 1 : ~0ull) & (a < 64 ? ~0ull << a : 0ull);
-                    const uint32_t half[2] = {uint32_t(seen), uint32_t(seen >> 32)};
+                    const uint32_t a = rr.lo > at ? rr.lo - at : 0, b = rr.hi > at ? rr.hi - at : 0;
 #pragma unroll
-                    for (uint32_t c = 0; c < 64; ++c)
-                        if (!(half[c / 32] & (1u << (c % 32)))) x[c] = 0xff800000u;
+                    for (uint32_t g = 0; g < 4; ++g) {
+                        const uint32_t ga = a > 32 * g ? min(a - 32 * g, 32u) : 0, gb = b > 32 * g ? min(b - 32 * g, 32u) : 0;
+                        const uint32_t seen = uint32_t((1ull << gb) - 1) & uint32_t(~0ull << ga);
+#pragma unroll
+                        for (uint32_t c = 0; c < 32; ++c)
+                            if (!(seen & (1u << c))) x[32 * g + c] = 0xff800000u;
+                    }
                 }
                 float tops[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tops[c] = __uint_as_float(x[c]);
+                for (int c = 0; c < 4; ++c) tops[c] = max3(__uint_as_float(x[c]), __uint_as_float(x[c + 4]), __uint_as_float(x[c + 8]));
 #pragma unroll
-                for (int c = 4; c < 64; ++c) tops[c & 3] = fmaxf(tops[c & 3], __uint_as_float(x[c]));
+                for (int c = 12; c < 124; c += 8) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        tops[e] = max3(tops[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + e + 4]));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tops[e] = fmaxf(tops[e], __uint_as_float(x[124 + e]));
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * sc;
                 const bool grows = top > m + C::SLACK;
                 if (__any_sync(0xffffffffu, grows)) {
@@ -706,9 +715,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                     if (grows) m = top;
                     l *= c;
                     if (j > t.from) {
-                        // these scores are behind the product before the last one; the last may be under way
-                        if (!warp_wait(&aux->o_done[i], (o_uses - 1) & 1, aux, p.ctl)) return;
-                        tc_after();
+                        // the scores came behind the last product: the sums are at rest
                         for (uint32_t k = 0; k < d; k += 16) {
                             uint32_t o[16];
                             tc_ld16(o, o_at + k);
@@ -723,7 +730,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                 const uint64_t sc2 = f2(sc, sc), shift2 = f2(shift, shift);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
+                for (int c = 0; c < 128; c += 32) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -734,17 +741,18 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                         sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2(a, b));
                         pk[e / 2] = DT == SZ_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
                     }
-                    tc_st16(s_at + buf * 64 + c / 2, pk);
+                    tc_st16(s_at + c / 2, pk);
+                    if (c & 32) {
+                        tc_wait_st();
+                        tc_before();
+                        bar_arrive(&aux->p_full[i][c / 64]);
+                    }
                 }
-                tc_wait_st();
-                tc_before();
-                bar_arrive(&aux->p_full[i][buf]);
-                ++o_uses;
                 float a, b;
                 f2_split(f2_add(sum[0], sum[1]), a, b);
                 l += a + b;
             }
-            if (!warp_wait(&aux->o_last[i], o_parts++ & 1, aux, p.ctl)) return;
+            if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p.ctl)) return;
             tc_after();
             if (whole_tile) {
                 const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
@@ -820,12 +828,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&aux->q_full[i], 32 * kQueryWarps);
             mbar_init(&aux->q_empty[i], 1 + 4);  // the products, and the warps of the tile's softmax
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&aux->s_full[i][b], 1);
-                mbar_init(&aux->p_full[i][b], 128);
-            }
-            mbar_init(&aux->o_done[i], 1);
-            mbar_init(&aux->o_last[i], 1);
+            mbar_init(&aux->s_full[i], 1);
+            for (int h = 0; h < 2; ++h) mbar_init(&aux->p_full[i][h], 128);
+            mbar_init(&aux->o_full[i], 1);
         }
         mbar_init(&aux->drain[0], 1);
         mbar_init(&aux->drain[1], 1);
