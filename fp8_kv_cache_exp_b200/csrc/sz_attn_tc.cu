@@ -41,6 +41,8 @@
 // several CTAs share, spread over all SMs.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "sz_attn.cuh"
 
 namespace sz {
@@ -48,6 +50,9 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
+#ifndef SZ_TURN
+#define SZ_TURN 64
+#endif
 constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;
 constexpr int kTcBlock = 128;
@@ -84,6 +89,7 @@ struct TcAux {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2][2];  // a tile's scores; the halves of its weights
     uint64_t o_full[2];                // a tile's sums, at the end of a part
+    uint64_t turn[2];                  // a tile's turn at ex2
     uint64_t drain[2];
     uint32_t tmem, abort, bad;
     int8_t exp[kTcRows];  // E5M2: exponent taken out of each query row
@@ -186,6 +192,12 @@ __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t *r) {
             SZ_I16(r, 0), "r"(a) : "memory");
 }
 
+// What a load brings is there only behind the wait: uses stay behind it too.
+__device__ __forceinline__ void tc_arrived(uint32_t *r) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                      "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 // Shared-memory descriptor of rows of 128 bytes, 8 rows to a swizzle atom:
 // leading offset (from one 64-element panel to the next; only values, whose
 // rows run along the result's columns, have a use for it), stride offset of
@@ -237,6 +249,34 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^x of two numbers of at most 127 without ex2, NaN for NaN.  x = n + f with n
+// whole and |f| <= 1/2: n by adding 1.5 2^23 (its last bits are then n, and 127
+// more what an exponent holds), 2^f by the polynomial of degree 4 with the
+// smallest largest relative error, 2^-18.5 (found by Remez's exchange).  Below
+// 2^-126 the result is 2^-126, not 0.
+__device__ __forceinline__ uint64_t f2_exp2(uint64_t x2) {
+    constexpr float kShift = 12582912.f + 127.f;
+    float a, b;
+    f2_split(x2, a, b);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-126.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-126.f));
+    x2 = f2(a, b);
+    const uint64_t t = f2_add(x2, f2(kShift, kShift));
+    const uint64_t n = f2_add(t, f2(-kShift, -kShift));
+    const uint64_t f = f2_fma(n, f2(-1.f, -1.f), x2);
+    uint64_t y = f2_fma(f2(0.009570102207362652f, 0.009570102207362652f), f, f2(0.05591785907745361f, 0.05591785907745361f));
+    y = f2_fma(y, f, f2(0.240247443318367f, 0.240247443318367f));
+    y = f2_fma(y, f, f2(0.6931217908859253f, 0.6931217908859253f));
+    y = f2_fma(y, f, f2(0.9999992847442627f, 0.9999992847442627f));
+    f2_split(t, a, b);
+    return f2_mul(y, f2(__uint_as_float(__float_as_uint(a) << 23), __uint_as_float(__float_as_uint(b) << 23)));
 }
 
 // ------------------------------------------------------------------- roles
@@ -584,28 +624,17 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
         return ok;
     };
     auto stage = [&](uint32_t n) { return smem_desc(base + C::RING_AT + (n % C::STAGES) * C::STAGE); };
-    // scores of the block with keys in stage n; the stage is free behind them, the queries if they are the last
-    auto qk = [&](uint32_t n, bool last) {
-        const uint64_t kd = stage(n);
-        if (leader) {
+    auto qk = [&](uint64_t kd) {
 #pragma unroll
-            for (uint32_t k = 0; k < DP / 16; ++k)
-                if (k < ksteps)
-                    mma_ss(i * 128, qd + (((k / 4) * kQPanel + (k % 4) * 32) >> 4),
-                           kd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), qk_desc, k > 0);
-            tc_commit(&aux->s_full[i]);
-            tc_commit(&aux->empty[n % C::STAGES]);
-            if (last) tc_commit(&aux->q_empty[i]);
-        }
-        __syncwarp();
+        for (uint32_t k = 0; k < DP / 16; ++k)
+            if (k < ksteps)
+                mma_ss(i * 128, qd + (((k / 4) * kQPanel + (k % 4) * 32) >> 4),
+                       kd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), qk_desc, k > 0);
     };
     auto pv = [&](uint32_t half, uint64_t vd, bool add) {
-        if (leader) {
 #pragma unroll
-            for (uint32_t k = half * 4; k < half * 4 + 4; ++k)
-                mma_ts(256 + i * 128, i * 128 + k * 8, vd + k * (2048 >> 4), pv_desc, add || k > 0);
-        }
-        __syncwarp();
+        for (uint32_t k = half * 4; k < half * 4 + 4; ++k)
+            mma_ts(256 + i * 128, i * 128 + k * 8, vd + k * (2048 >> 4), pv_desc, add || k > 0);
     };
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
@@ -613,24 +642,38 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
         if (i * 128 < t.rows) {
             if (!full(kv)) return;
             if (!wait(&aux->q_full[i], 2)) return;
-            qk(kv, n == 1);
+            if (leader) {
+                qk(stage(kv));
+                tc_commit(&aux->s_full[i]);
+                tc_commit(&aux->empty[kv % C::STAGES]);
+                if (n == 1) tc_commit(&aux->q_empty[i]);
+            }
+            __syncwarp();
             for (uint32_t j = 0; j < n; ++j) {
                 const uint32_t v = kv + 2 * j + 1, k = v + 1;
-                const uint64_t vd = stage(v);
+                const uint64_t vd = stage(v), kd = stage(k);
                 if (!full(v)) return;
                 if (!wait(&aux->p_full[i][0], 0)) return;
-                pv(0, vd, j > 0);
+                if (leader) pv(0, vd, j > 0);
+                __syncwarp();
+                // what the second half's way to the next scores does not depend on comes before it, or behind
+                const bool more = j + 1 < n;
+                if (more && !full(k)) return;
                 if (!wait(&aux->p_full[i][1], 1)) return;
-                pv(1, vd, true);
                 if (leader) {
-                    tc_commit(&aux->empty[v % C::STAGES]);
-                    if (j + 1 == n) tc_commit(&aux->o_full[i]);
+                    pv(1, vd, true);
+                    if (more) {
+                        qk(kd);
+                        tc_commit(&aux->s_full[i]);
+                        tc_commit(&aux->empty[v % C::STAGES]);
+                        tc_commit(&aux->empty[k % C::STAGES]);
+                        if (j + 2 == n) tc_commit(&aux->q_empty[i]);
+                    } else {
+                        tc_commit(&aux->o_full[i]);
+                        tc_commit(&aux->empty[v % C::STAGES]);
+                    }
                 }
                 __syncwarp();
-                if (j + 1 < n) {
-                    if (!full(k)) return;
-                    qk(k, j + 2 == n);
-                }
             }
         } else {
             // the other tile's stages need this one's word too
@@ -653,7 +696,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
     const uint32_t lanes = (threadIdx.x & 96) << 16;  // the warp's quarter of tensor memory
     const uint32_t s_at = lanes + i * 128, o_at = lanes + 256 + i * 128;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    uint32_t q_uses = 0, s_uses = 0, o_uses = 0;
+    uint32_t q_uses = 0, s_uses = 0, o_uses = 0, turns = 0;
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const bool whole_tile = t.c_first == t.c_last;
@@ -678,33 +721,49 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
             for (uint32_t j = t.from; j < t.to; ++j) {
                 if (!warp_wait(&aux->s_full[i], s_uses++ & 1, aux, p.ctl)) return;
                 tc_after();
+                const uint32_t at = (t.block0 + j) * kTcBlock;
+                const bool masked = at < full_lo || at + kTcBlock > full_hi;
                 uint32_t x[128];
+                if (masked) {
+                    // columns [a, b) of the block are seen; the others' scores become -infinity where they are
+                    const uint32_t a = rr.lo > at ? rr.lo - at : 0, b = rr.hi > at ? rr.hi - at : 0;
+                    for (uint32_t g = 0; g < 128; g += 16) {
+                        tc_ld16(x, s_at + g);
+                        tc_wait_ld();
+                        tc_arrived(x);
+                        const uint32_t ga = a > g ? min(a - g, 16u) : 0, gb = b > g ? min(b - g, 16u) : 0;
+                        const uint32_t seen = ((1u << gb) - 1) & (~0u << ga);
+#pragma unroll
+                        for (uint32_t c = 0; c < 16; ++c)
+                            if (!(seen & (1u << c))) x[c] = 0xff800000u;
+                        tc_st16(s_at + g, x);
+                    }
+                    tc_wait_st();
+                }
                 tc_ld32(x, s_at);
                 tc_ld32(x + 32, s_at + 32);
+                tc_wait_ld();
                 tc_ld32(x + 64, s_at + 64);
                 tc_ld32(x + 96, s_at + 96);
-                tc_wait_ld();
-                const uint32_t at = (t.block0 + j) * kTcBlock;
-                if (at < full_lo || at + kTcBlock > full_hi) {
-                    // columns [a, b) of the block are seen
-                    const uint32_t a = rr.lo > at ? rr.lo - at : 0, b = rr.hi > at ? rr.hi - at : 0;
+                // (the first half's maximum while the second half comes)
 #pragma unroll
-                    for (uint32_t g = 0; g < 4; ++g) {
-                        const uint32_t ga = a > 32 * g ? min(a - 32 * g, 32u) : 0, gb = b > 32 * g ? min(b - 32 * g, 32u) : 0;
-                        const uint32_t seen = uint32_t((1ull << gb) - 1) & uint32_t(~0ull << ga);
-#pragma unroll
-                        for (uint32_t c = 0; c < 32; ++c)
-                            if (!(seen & (1u << c))) x[32 * g + c] = 0xff800000u;
-                    }
-                }
+                for (int c = 0; c < 64; c += 16) tc_arrived(x + c);
                 float tops[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tops[c] = max3(__uint_as_float(x[c]), __uint_as_float(x[c + 4]), __uint_as_float(x[c + 8]));
+                for (int e = 0; e < 4; ++e)
+                    tops[e] = max3(__uint_as_float(x[e]), __uint_as_float(x[e + 4]), __uint_as_float(x[e + 8]));
 #pragma unroll
-                for (int c = 12; c < 124; c += 8) {
+                for (int c = 12; c < 60; c += 8) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        tops[e] = max3(tops[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + e + 4]));
+                    for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + e + 4]));
+                }
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 64; c < 128; c += 16) tc_arrived(x + c);
+#pragma unroll
+                for (int c = 60; c < 124; c += 8) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + e + 4]));
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) tops[e] = fmaxf(tops[e], __uint_as_float(x[124 + e]));
@@ -726,31 +785,56 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                         }
                     }
                 }
+                // The tiles take turns at ex2: side by side they would both wait for
+                // it, and then both for their products.
+                if (t.rows > 128) {
+                    if ((i == 1 || turns > 0) && !warp_wait(&aux->turn[i], (turns - 1 + i) & 1, aux, p.ctl)) return;
+                    ++turns;
+                }
                 const float shift = C::RAISE - (m == -INFINITY ? 0.f : m);
                 const uint64_t sc2 = f2(sc, sc), shift2 = f2(shift, shift);
                 uint64_t sum[2] = {0, 0};
+                // Of a block that all rows see whole, 6 of 16 pairs take the polynomial, so that
+                // ex2 (8 clocks of a warp) and multiply-adds (16 for such a pair) end together.
+                auto weights = [&](auto mixed) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t pk[16];
+                    for (int c = 0; c < 128; c += 32) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float a, b;
-                        f2_split(f2_fma(f2(__uint_as_float(x[c + e]), __uint_as_float(x[c + e + 1])), sc2, shift2), a, b);
-                        a = exp2_fast(a);
-                        b = exp2_fast(b);
-                        sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2(a, b));
-                        pk[e / 2] = DT == SZ_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
+                        for (int e = 0; e < 32; e += 2) {
+                            const uint64_t y = f2_fma(f2(__uint_as_float(x[c + e]), __uint_as_float(x[c + e + 1])), sc2, shift2);
+                            float a, b;
+                            if (decltype(mixed)::value && ((0xA4A4 >> (e / 2)) & 1)) {
+                                const uint64_t z = f2_exp2(y);
+                                f2_split(z, a, b);
+                                sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], z);
+                            } else {
+                                f2_split(y, a, b);
+                                a = exp2_fast(a);
+                                b = exp2_fast(b);
+                                sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2(a, b));
+                            }
+                            pk[e / 2] = DT == SZ_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
+                        }
+                        tc_st16(s_at + c / 2, pk);
+                        if (c == SZ_TURN && t.rows > 128) {
+                            __syncwarp();
+                            if ((threadIdx.x & 31) == 0) bar_arrive(&aux->turn[1 - i]);
+                            __syncwarp();
+                        }
+                        if (c & 32) {
+                            tc_wait_st();
+                            tc_before();
+                            bar_arrive(&aux->p_full[i][c / 64]);
+                        }
                     }
-                    tc_st16(s_at + c / 2, pk);
-                    if (c & 32) {
-                        tc_wait_st();
-                        tc_before();
-                        bar_arrive(&aux->p_full[i][c / 64]);
-                    }
-                }
+                };
+                // (a place that a row does not see weighs 0, not next to nothing)
+                if (masked) weights(std::false_type{});
+                else weights(std::true_type{});
                 float a, b;
                 f2_split(f2_add(sum[0], sum[1]), a, b);
-                l += a + b;
+                l = m == -INFINITY ? 0.f : l + (a + b);
             }
             if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p.ctl)) return;
             tc_after();
@@ -831,6 +915,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&aux->s_full[i], 1);
             for (int h = 0; h < 2; ++h) mbar_init(&aux->p_full[i][h], 128);
             mbar_init(&aux->o_full[i], 1);
+            mbar_init(&aux->turn[i], 4);
         }
         mbar_init(&aux->drain[0], 1);
         mbar_init(&aux->drain[1], 1);
