@@ -37,11 +37,10 @@
 // upper byte) on their way to that layout; queries are then fp16 too, behind a
 // power of two for each row that brings the row's largest below 2^14.
 //
-// A second kernel, which starts as the first one ends, joins the tiles that
-// several CTAs share, spread over all SMs.
+// A tile that a few CTAs share is joined by the last of them; one that many
+// share (long contexts of few rows) by a second kernel, which starts as the first
+// one ends and spreads the sums over all SMs.
 #include <cuda.h>
-
-#include <type_traits>
 
 #include "sz_attn.cuh"
 
@@ -50,12 +49,10 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
-#ifndef SZ_TURN
-#define SZ_TURN 64
-#endif
 constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;
 constexpr int kTcBlock = 128;
+constexpr uint32_t kFewParts = 4;             // a tile of so many parts is joined by the last of them
 constexpr uint32_t kQPanel = 128 * 128;       // bytes of 128 rows of 64 16-bit elements
 constexpr uint32_t kPanel = kTcBlock * 128;   // of a block's rows
 // registers of a softmax thread and of the others: 256 * 192 + 256 * 64 = 512 * 128,
@@ -86,7 +83,7 @@ struct TcCfg {
 struct TcAux {
     uint64_t full[10], empty[10];
     uint64_t raw_full[8], raw_empty[8];
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[2], q_empty[2], q_here[2];  // (q_here: E5M2, queries as they come)
     uint64_t s_full[2], p_full[2][2];  // a tile's scores; the halves of its weights
     uint64_t o_full[2];                // a tile's sums, at the end of a part
     uint64_t turn[2];                  // a tile's turn at ex2
@@ -141,6 +138,14 @@ __device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap *map,
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
         "[%6];" ::"r"(dst),
         "l"(map), "r"(x), "r"(head), "r"(token), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tensor3_g2s(uint32_t dst, const CUtensorMap *map, uint32_t x, uint32_t y, uint32_t z,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -249,34 +254,6 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// 2^x of two numbers of at most 127 without ex2, NaN for NaN.  x = n + f with n
-// whole and |f| <= 1/2: n by adding 1.5 2^23 (its last bits are then n, and 127
-// more what an exponent holds), 2^f by the polynomial of degree 4 with the
-// smallest largest relative error, 2^-18.5 (found by Remez's exchange).  Below
-// 2^-126 the result is 2^-126, not 0.
-__device__ __forceinline__ uint64_t f2_exp2(uint64_t x2) {
-    constexpr float kShift = 12582912.f + 127.f;
-    float a, b;
-    f2_split(x2, a, b);
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-126.f));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-126.f));
-    x2 = f2(a, b);
-    const uint64_t t = f2_add(x2, f2(kShift, kShift));
-    const uint64_t n = f2_add(t, f2(-kShift, -kShift));
-    const uint64_t f = f2_fma(n, f2(-1.f, -1.f), x2);
-    uint64_t y = f2_fma(f2(0.009570102207362652f, 0.009570102207362652f), f, f2(0.05591785907745361f, 0.05591785907745361f));
-    y = f2_fma(y, f, f2(0.240247443318367f, 0.240247443318367f));
-    y = f2_fma(y, f, f2(0.6931217908859253f, 0.6931217908859253f));
-    y = f2_fma(y, f, f2(0.9999992847442627f, 0.9999992847442627f));
-    f2_split(t, a, b);
-    return f2_mul(y, f2(__uint_as_float(__float_as_uint(a) << 23), __uint_as_float(__float_as_uint(b) << 23)));
 }
 
 // ------------------------------------------------------------------- roles
@@ -525,43 +502,66 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
     }
 }
 
-// Queries into shared memory (warps 14, 15).
+// Queries into shared memory (warps 14, 15): by tensor copies of 128 / G tokens
+// of the group's G heads where G divides 128 (`map`; rows behind the sequence's
+// last are then the next one's, and nobody's), or row by row.
 constexpr uint32_t kQueryWarps = 2;
 template <int DT, int DP>
-__device__ __forceinline__ void query_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux) {
+__device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMap *map, Work w, uint32_t base, TcAux *aux) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t QL = DP / 8, QR = 32 / QL;          // lanes to a row, rows to an instruction
     constexpr uint32_t BATCH = 8;
     const uint32_t lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 14, c = lane % QL;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i]
+    uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i]; bit 2 + i: of q_here[i]
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const uint8_t *q = p.q.p + uint64_t(t.s.q0) * p.q.ts + uint64_t(w.head * G) * p.q.hs;
         for (uint32_t i = 0; i * 128 < t.rows; ++i) {
             if (seen & (1u << i)) {
-                if (!warp_wait(&aux->q_empty[i], (phases >> i) & 1, aux, p.ctl)) return;
+                if (!warp_wait(&aux->q_empty[i], (phases >> i) & 1, aux, p.ctl)) {
+                    // giving up: tensor copies that are under way land, or a limit passes
+                    for (uint32_t x = 0; DT == SZ_BF16 && map && x < 2; ++x)
+                        for (uint32_t n = 0; (seen >> x & 1) && n < 1u << 16 && !mbar_try_wait(&aux->q_full[x], (phases >> x) & 1); ++n) {}
+                    return;
+                }
                 phases ^= 1u << i;
             }
             seen |= 1u << i;
             const uint32_t tile = base + i * C::QTILE + (c / 8) * kQPanel;
-            for (uint32_t r0 = warp * BATCH * QR; r0 < 128; r0 += kQueryWarps * BATCH * QR) {
-                // a lane finds one row; rows behind the last are zeros
-                const uint32_t mine = i * 128 + r0 + lane % (BATCH * QR);
-                uint64_t at = kBadOffset;
-                if (mine < t.rows) {
-                    const uint32_t g = t.r0 + mine, tok = div_by(g, p.group);
-                    at = uint64_t(tok) * p.q.ts + uint64_t(g - tok * G) * p.q.hs;
+            if (map) {
+                uint64_t *bar = DT == SZ_BF16 ? &aux->q_full[i] : &aux->q_here[i];
+                if (warp == 0 && lane == 0) {
+                    mbar_arrive_expect_tx(bar, C::QTILE);
+                    const uint32_t token = t.s.q0 + div_by(t.r0 + i * 128, p.group);
+                    for (uint32_t x = 0; x < C::PANELS; ++x)
+                        tensor3_g2s(base + i * C::QTILE + x * kQPanel, map, x * 64, w.head * G, token, bar);
+                } else if (DT == SZ_BF16) {
+                    bar_arrive(bar);
                 }
-                uint64_t o[BATCH];
+                __syncwarp();
+                if constexpr (DT == SZ_BF16) continue;
+                if (!warp_wait(bar, (phases >> (2 + i)) & 1, aux, p.ctl)) return;
+                phases ^= 1u << (2 + i);
+            } else {
+                for (uint32_t r0 = warp * BATCH * QR; r0 < 128; r0 += kQueryWarps * BATCH * QR) {
+                    // a lane finds one row; rows behind the last are zeros
+                    const uint32_t mine = i * 128 + r0 + lane % (BATCH * QR);
+                    uint64_t at = kBadOffset;
+                    if (mine < t.rows) {
+                        const uint32_t g = t.r0 + mine, tok = div_by(g, p.group);
+                        at = uint64_t(tok) * p.q.ts + uint64_t(g - tok * G) * p.q.hs;
+                    }
+                    uint64_t o[BATCH];
 #pragma unroll
-                for (uint32_t u = 0; u < BATCH; ++u) o[u] = __shfl_sync(0xffffffffu, at, int(u * QR + lane / QL));
-                if (c * 8 < d) {
+                    for (uint32_t u = 0; u < BATCH; ++u) o[u] = __shfl_sync(0xffffffffu, at, int(u * QR + lane / QL));
+                    if (c * 8 < d) {
 #pragma unroll
-                    for (uint32_t u = 0; u < BATCH; ++u) {
-                        const uint32_t r = r0 + u * QR + lane / QL;
-                        const bool in = o[u] != kBadOffset;
-                        cp_async16(tile + r * 128 + (((c % 8) ^ (r & 7)) << 4), in ? q + o[u] + c * 16 : p.q.p, in);
+                        for (uint32_t u = 0; u < BATCH; ++u) {
+                            const uint32_t r = r0 + u * QR + lane / QL;
+                            const bool in = o[u] != kBadOffset;
+                            cp_async16(tile + r * 128 + (((c % 8) ^ (r & 7)) << 4), in ? q + o[u] + c * 16 : p.q.p, in);
+                        }
                     }
                 }
             }
@@ -688,6 +688,71 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
     }
 }
 
+// A warp's 32 rows of a tile with few parts: the warp that comes last to them
+// adds them up, in the parts' order.
+template <int DT>
+__device__ __forceinline__ void join_few(const AttnParams &p, const Work &w, const Part &t, uint32_t r, uint32_t parts,
+                                         TcAux *aux) {
+    constexpr float RAISE = TcCfg<DT, 64>::RAISE;
+    const uint32_t d = p.cache.head_dim, lane = threadIdx.x & 31;
+    uint32_t *arrived = p.arrived + t.c_first * 8 + r / 32;
+    __threadfence();
+    __syncwarp();
+    uint32_t n = 0;
+    if (lane == 0) n = atomicAdd(arrived, 1u);
+    if (__shfl_sync(0xffffffffu, n, 0) != parts - 1) return;
+    __threadfence();
+    if (lane == 0) *arrived = 0;
+    const float *from[kFewParts];
+    float f[kFewParts], M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (uint32_t k = 0; k < kFewParts; ++k) {
+        from[k] = p.part + uint64_t(part_slot(t.c_first + min(k, parts - 1), t)) * kTcRows * (d + 2);
+        f[k] = k < parts ? __ldcg(from[k] + d * kTcRows + r) : -INFINITY;
+        M = fmaxf(M, f[k]);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kFewParts; ++k) {
+        f[k] = exp2_fast(f[k] - (M == -INFINITY ? 0.f : M));
+        if (k < parts) L = fmaf(f[k], __ldcg(from[k] + (d + 1) * kTcRows + r), L);
+    }
+    const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * p.group.d + (g - tok * p.group.d);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs;
+    float worst = 0.f;
+    for (uint32_t e = 0; e < d; e += 16) {
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+#pragma unroll
+        for (uint32_t k = 0; k < kFewParts; ++k) {
+            if (k >= parts) break;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(from[k]) + ((e + j) / 4 * kTcRows + r));
+                v[j] = fmaf(f[k], x.x, v[j]), v[j + 1] = fmaf(f[k], x.y, v[j + 1]);
+                v[j + 2] = fmaf(f[k], x.z, v[j + 2]), v[j + 3] = fmaf(f[k], x.w, v[j + 3]);
+            }
+        }
+        uint32_t pk[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[2 * j] *= inv, v[2 * j + 1] *= inv;
+            worst = fmaf(0.f, v[2 * j], fmaf(0.f, v[2 * j + 1], worst));  // stays 0, or is NaN
+            pk[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+        }
+        if (r < t.rows) {
+            *reinterpret_cast<uint4 *>(out + 2 * e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4 *>(out + 2 * e + 16) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        }
+    }
+    if (r < t.rows) {
+        if (p.lse)
+            p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] = L == 0.f ? -INFINITY : kLn2 * (M - RAISE + log2f(L));
+        if (worst != 0.f) aux->bad = 1;
+    }
+}
+
 // Softmax of one tile's rows, a thread a row, and what becomes of the sums.
 template <int DT, int DP>
 __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux *aux, TcDesc *desc) {
@@ -700,7 +765,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const bool whole_tile = t.c_first == t.c_last;
-        if (threadIdx.x == 0 && !whole_tile && t.c_first == blockIdx.x) {
+        const uint32_t parts = t.c_last - t.c_first + 1;
+        if (threadIdx.x == 0 && parts > kFewParts && t.c_first == blockIdx.x) {
             desc->join = w;
             desc->joins = 1;
         }
@@ -785,8 +851,11 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                         }
                     }
                 }
-                // The tiles take turns at ex2: side by side they would both wait for
-                // it, and then both for their products.
+                // The tiles take turns at ex2, three quarters of a block apart: side by
+                // side they would both wait for it, and then both for their products
+                // (2048-token chunk: 308 us; by turns 242).  A polynomial in place of a
+                // part of the ex2 made it 255: its multiply-adds, two to an instruction
+                // or not, take the issue slots.
                 if (t.rows > 128) {
                     if ((i == 1 || turns > 0) && !warp_wait(&aux->turn[i], (turns - 1 + i) & 1, aux, p.ctl)) return;
                     ++turns;
@@ -794,47 +863,37 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                 const float shift = C::RAISE - (m == -INFINITY ? 0.f : m);
                 const uint64_t sc2 = f2(sc, sc), shift2 = f2(shift, shift);
                 uint64_t sum[2] = {0, 0};
-                // Of a block that all rows see whole, 6 of 16 pairs take the polynomial, so that
-                // ex2 (8 clocks of a warp) and multiply-adds (16 for such a pair) end together.
-                auto weights = [&](auto mixed) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        uint32_t pk[16];
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const uint64_t y = f2_fma(f2(__uint_as_float(x[c + e]), __uint_as_float(x[c + e + 1])), sc2, shift2);
-                            float a, b;
-                            if (decltype(mixed)::value && ((0xA4A4 >> (e / 2)) & 1)) {
-                                const uint64_t z = f2_exp2(y);
-                                f2_split(z, a, b);
-                                sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], z);
-                            } else {
-                                f2_split(y, a, b);
-                                a = exp2_fast(a);
-                                b = exp2_fast(b);
-                                sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2(a, b));
-                            }
-                            pk[e / 2] = DT == SZ_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
-                        }
-                        tc_st16(s_at + c / 2, pk);
-                        if (c == SZ_TURN && t.rows > 128) {
-                            __syncwarp();
-                            if ((threadIdx.x & 31) == 0) bar_arrive(&aux->turn[1 - i]);
-                            __syncwarp();
-                        }
-                        if (c & 32) {
-                            tc_wait_st();
-                            tc_before();
-                            bar_arrive(&aux->p_full[i][c / 64]);
-                        }
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, b;
+                        f2_split(f2_fma(f2(__uint_as_float(x[c + e]), __uint_as_float(x[c + e + 1])), sc2, shift2), a, b);
+                        a = exp2_fast(a);
+                        b = exp2_fast(b);
+                        sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2(a, b));
+                        pk[e / 2] = DT == SZ_BF16 ? pack_bf16(a, b) : pack_f16(a, b);
                     }
-                };
-                // (a place that a row does not see weighs 0, not next to nothing)
-                if (masked) weights(std::false_type{});
-                else weights(std::true_type{});
+                    if (c == 64) {
+                        // the first half has long been stored by now
+                        tc_wait_st();
+                        tc_before();
+                        bar_arrive(&aux->p_full[i][0]);
+                    }
+                    tc_st16(s_at + c / 2, pk);
+                    if (c == 64 && t.rows > 128) {
+                        __syncwarp();
+                        if ((threadIdx.x & 31) == 0) bar_arrive(&aux->turn[1 - i]);
+                        __syncwarp();
+                    }
+                }
+                tc_wait_st();
+                tc_before();
+                bar_arrive(&aux->p_full[i][1]);
                 float a, b;
                 f2_split(f2_add(sum[0], sum[1]), a, b);
-                l = m == -INFINITY ? 0.f : l + (a + b);
+                l += a + b;
             }
             if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p.ctl)) return;
             tc_after();
@@ -880,6 +939,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                 }
                 part[d * kTcRows] = m;
                 part[(d + 1) * kTcRows] = l;
+                if (parts <= kFewParts) join_few<DT>(p, w, t, r, parts, aux);
             }
             // the sums are read before the next part's first weights are announced
             tc_before();
@@ -891,7 +951,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
 template <int DT, int DP>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map,
-                   const __grid_constant__ CUtensorMap v_map, uint32_t box) {
+                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map, uint32_t box,
+                   uint32_t q_box) {
     using C = TcCfg<DT, DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -911,6 +972,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&aux->q_full[i], 32 * kQueryWarps);
+            mbar_init(&aux->q_here[i], 1);
             mbar_init(&aux->q_empty[i], 1 + 4);  // the products, and the warps of the tile's softmax
             mbar_init(&aux->s_full[i], 1);
             for (int h = 0; h < 2; ++h) mbar_init(&aux->p_full[i][h], 128);
@@ -963,7 +1025,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             warp_wait(&aux->drain[warp - 12], 0, aux, p.ctl);
         } else {
-            query_role<DT, DP>(p, w, base, aux);
+            query_role<DT, DP>(p, q_box ? &q_map : nullptr, w, base, aux);
             cp_wait<0>();
         }
     }
@@ -983,9 +1045,9 @@ constexpr int kJoinSlices = kTcRows / kJoinRows;
 constexpr uint32_t kJoinWarps = kJoinThreads / 32;
 constexpr uint32_t kJoinSplit = 4;                        // groups of columns ...
 constexpr uint32_t kJoinGroups = kJoinWarps / kJoinSplit; // ... and of parts
+static_assert(kMaxSms <= kJoinThreads, "a thread looks at a CTA");
 
-// CTA (c, slice): 32 rows of the tile that CTA c began and others ended, a lane
-// a row; a warp has a quarter of the columns of every second part.
+// Tiles of more than kFewParts parts; an item is 32 rows of one, a lane a row; a warp has a quarter of the columns of every second part.
 template <int DT, int DP>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p) {
     using C = TcCfg<DT, DP>;
@@ -995,15 +1057,30 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     __shared__ uint32_t s_bad;
     pdl_wait();
     pdl_launch_dependents();
-    const uint32_t c = blockIdx.x / kJoinSlices, slice = blockIdx.x % kJoinSlices;
+    __shared__ uint32_t s_list[kJoinWarps][33];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    const TcDesc *desc = reinterpret_cast<const TcDesc *>(p.desc) + c;
-    if (!desc->has) return;
-    if (desc->joins) {
-        const Work w = desc->join;
+    const TcDesc *descs = reinterpret_cast<const TcDesc *>(p.desc);
+    // the tiles to join, listed by each warp for its 32 of the CTAs
+    {
+        const bool joins = threadIdx.x < gridDim.x && descs[threadIdx.x].has && descs[threadIdx.x].joins;
+        const uint32_t all = __ballot_sync(0xffffffffu, joins);
+        if (joins) s_list[warp][1 + __popc(all & lanemask_lt())] = threadIdx.x;
+        if (lane == 0) s_list[warp][0] = __popc(all);
+    }
+    __syncthreads();
+    uint32_t tiles = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < kJoinWarps; ++k) tiles += s_list[k][0];
+    for (uint32_t item = blockIdx.x; item < tiles * kJoinSlices; item += gridDim.x) {
+        const uint32_t slice = item % kJoinSlices;
+        uint32_t k = 0, nth = item / kJoinSlices;
+        while (nth >= s_list[k][0]) nth -= s_list[k++][0];
+        const uint32_t c = s_list[k][1 + nth];
+        const Work w = descs[c].join;
         const Part t = work_part<kTcRows, kTcBlock>(p, w, c);
         if (slice * kJoinRows < t.rows) {
+            __syncthreads();  // (the last item's sums are read)
             const uint32_t r = slice * kJoinRows + lane, parts = t.c_last - t.c_first + 1;
             if (threadIdx.x == 0) s_bad = 0;
             auto slot = [&](uint32_t k) {
@@ -1078,13 +1155,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             }
         }
     }
-    if (desc->bad) {
-        // rows of the CTA's own tiles that are not finite
-        Work w = desc->begin;
+    const uint32_t c = blockIdx.x;
+    if (descs[c].has && descs[c].bad) {
+        // rows that are not finite of the tiles that the CTA had alone, or joined
+        Work w = descs[c].begin;
         for (;;) {
             const Part t = work_part<kTcRows, kTcBlock>(p, w, c);
-            if (t.c_first == t.c_last)
-                for (uint32_t r = slice * (kJoinThreads / 32) + warp; r < t.rows; r += kJoinSlices * (kJoinThreads / 32)) {
+            if (t.c_last - t.c_first < kFewParts)
+                for (uint32_t r = warp; r < t.rows; r += kJoinWarps) {
                     const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
                     const uint16_t *out = reinterpret_cast<const uint16_t *>(
                         p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs);
@@ -1130,6 +1208,21 @@ bool pool_map(CUtensorMap *map, const AttnParams &p, uint8_t *pool, uint32_t box
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries as [tokens, heads, head_dim]; boxes of 128 / G tokens of G heads.
+bool query_map(CUtensorMap *map, const AttnParams &p) {
+    const EncodeTiled encode = encode_tiled();
+    const uint32_t G = p.group.d;
+    // (one token or one head: its stride is nothing that a map takes)
+    const uint64_t hs = p.q.heads > 1 ? p.q.hs : uint64_t(p.cache.head_dim) * 2;
+    const uint64_t ts = p.tokens > 1 ? p.q.ts : hs * p.q.heads;
+    if (!encode || G > 128 || 128 % G != 0 || hs == 0 || ts == 0 || hs >= (1ull << 40) || ts >= (1ull << 40)) return false;
+    const cuuint64_t dims[3] = {p.cache.head_dim, p.q.heads, p.tokens}, strides[2] = {hs, ts};
+    const cuuint32_t boxes[3] = {64, G, 128 / G}, one[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.q.p, dims, strides, boxes, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DT, int DP>
 sz_status run(const AttnParams &p, int num_sms, cudaStream_t stream) {
     using C = TcCfg<DT, DP>;
@@ -1137,13 +1230,14 @@ sz_status run(const AttnParams &p, int num_sms, cudaStream_t stream) {
     auto kern = attn_tc_kernel<DT, DP>;
     if (resident_per_sm(reinterpret_cast<const void *>(kern), kTcThreads, C::SMEM, cache) <= 0) return SZ_ERR_CUDA;
     // rows of a box: the largest power of two that divides a page, from 8 (a swizzle atom) to a block
-    CUtensorMap k_map{}, v_map{};
+    CUtensorMap k_map{}, v_map{}, q_map{};
     uint32_t box = p.cache.page_tokens.d & (0u - p.cache.page_tokens.d);
     box = box < 8 ? 0 : (box < uint32_t(kTcBlock) ? box : uint32_t(kTcBlock));
     if (box && !(pool_map<DT, DP>(&k_map, p, p.cache.k, box) && pool_map<DT, DP>(&v_map, p, p.cache.v, box))) box = 0;
-    if (launch_pdl(kern, unsigned(num_sms), kTcThreads, C::SMEM, stream, p, k_map, v_map, box) != cudaSuccess)
+    const uint32_t q_box = query_map(&q_map, p) ? 1 : 0;
+    if (launch_pdl(kern, unsigned(num_sms), kTcThreads, C::SMEM, stream, p, k_map, v_map, q_map, box, q_box) != cudaSuccess)
         return SZ_ERR_CUDA;
-    return launch_pdl(attn_join_kernel<DT, DP>, unsigned(num_sms) * kJoinSlices, kJoinThreads, 0, stream, p) ==
+    return launch_pdl(attn_join_kernel<DT, DP>, unsigned(num_sms), kJoinThreads, 0, stream, p) ==
                    cudaSuccess
                ? SZ_OK
                : SZ_ERR_CUDA;

@@ -62,7 +62,7 @@ struct RopeParams {
 
 struct AttnParams {
     uint32_t *ctl;
-    uint32_t *arrived;   // one counter for each CTA, zero between calls
+    uint32_t *arrived;   // arrival counters, zero between calls
     uint8_t *desc;       // what a CTA of the tensor-memory kernel leaves for the joining one
     float *part;         // partial results, two slots for each CTA
     CacheRef cache;
@@ -140,7 +140,8 @@ sz_status launch_attn_tc(const AttnParams &p, int dtype, int num_sms, cudaStream
 // sums in float and two statistics a row.
 constexpr uint32_t kMaxSms = 160;
 constexpr uint32_t kAttnCtas = 3 * kMaxSms;  // most CTAs of any attention kernel
-constexpr size_t kArrivedBytes = size_t(kAttnCtas) * 4;
+constexpr size_t kArrivedBytes = size_t(kMaxSms) * 8 * 4;  // the tensor-memory kernel counts for each warp of a tile
+static_assert(kAttnCtas <= kMaxSms * 8, "arrival counters");
 constexpr size_t kDescBytes = size_t(kMaxSms) * 128;
 // floats of all partials: the largest (CTAs * rows) of the kernels is a
 // persistent CTA for each SM with 256 rows, or kAttnCtas of 32
