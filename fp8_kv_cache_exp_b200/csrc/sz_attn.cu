@@ -24,6 +24,7 @@ constexpr int kSplitThreads = 128;
 constexpr int kSplitWarps = kSplitThreads / 32;
 constexpr int kPlaces = 16;  // places of a warp's step
 constexpr int kSplitBlock = 64;
+constexpr int kSplitExtra = 0;
 
 template <int DT, int DP, int MT>
 struct SplitCfg {
@@ -104,9 +105,9 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
     const bool has_piece = piece * 16 < d * C::EB;
 
     Work w;
-    if (!work_begin<kSplitThreads, TR, kSplitBlock>(p, s_work, w)) return;
+    if (!work_begin<kSplitThreads, TR, kSplitBlock, kSplitExtra>(p, s_work, w)) return;
     for (;;) {
-        const Part t = work_part<TR, kSplitBlock>(p, w, blockIdx.x);
+        const Part t = work_part<TR, kSplitBlock, kSplitExtra>(p, w, blockIdx.x);
         const int32_t *ids = p.cache.table + uint64_t(w.seq) * p.cache.table_stride;
         // places of this CTA's part, whole steps of 16 (lo down to a step's start)
         const uint32_t part_lo = max((t.block0 + t.from) * kSplitBlock, t.r.lo / kPlaces * kPlaces);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
                 if (s_bad[r]) repair_row<DT>(p, t.s, w.seq, w.head, t.r0 + r, t.r);
             __syncthreads();
         }
-        if (!work_next<TR>(p, w, t)) break;
+        if (!work_next<TR, kSplitExtra>(p, w, t)) break;
     }
 }
 

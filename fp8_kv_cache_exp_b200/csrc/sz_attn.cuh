@@ -7,7 +7,8 @@
 // work is counted in blocks of BN places that any of its rows sees.  The
 // blocks of all tiles, in the order (KV head, sequence, tile, block), are dealt
 // out evenly and in runs: CTA c of C has floor(U / C) of them, and one more if
-// c < U mod C.  A tile that
+// c < U mod C.  A tile counts EXTRA blocks more than it has, in front, for what
+// it costs besides them (queries to fetch, results to write).  A tile that
 // falls to several CTAs is joined from their partial results, in the order of
 // the CTAs, by the one that finishes last; so the result does not depend on
 // which one that is.
@@ -123,7 +124,7 @@ __device__ __forceinline__ uint64_t block_scan64(uint64_t v, uint64_t *s_warp, u
 }
 
 // The CTA's share; false if it has none.  All NT threads call it.
-template <int NT, int TR, int BN>
+template <int NT, int TR, int BN, int EXTRA>
 __device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w) {
     const uint32_t tid = threadIdx.x, seqs = p.cache.seqs;
     // this thread's tile of the chunk looked at last
@@ -164,7 +165,7 @@ __device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w) {
                     }
                     seq = sb + j;
                     tile = t - s.tp[j];
-                    units = range_blocks<BN>(tile_range<TR>(p, SeqInfo{0, s.q_len[j], s.kv[j]}, tile));
+                    units = EXTRA + range_blocks<BN>(tile_range<TR>(p, SeqInfo{0, s.q_len[j], s.kv[j]}, tile));
                 }
                 uint64_t sum;
                 before = run + block_scan64<NT>(units, s.warp, &sum);
@@ -192,7 +193,7 @@ __device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w) {
     w.tile = s.found[1];
     w.from = s.found[2];
     __syncthreads();
-    return true;
+    return w.from + (w.end - w.at) > EXTRA;
 }
 
 // The CTA that has a block.
@@ -209,10 +210,11 @@ struct Part {
     uint32_t rows, r0;      // rows of the tile, the first of them
     uint32_t block0;        // the tile's first block
     uint32_t from, to, n;
+    uint32_t count;         // of the share's blocks, the extra ones among them
     uint32_t c_first, c_last;  // CTAs that share the tile
 };
 
-template <int TR, int BN>
+template <int TR, int BN, int EXTRA>
 __device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w, uint32_t cta) {
     Part t;
     t.s = seq_info(p, w.seq);
@@ -221,12 +223,14 @@ __device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w, ui
     t.rows = min(uint32_t(TR), t.s.q_len * p.group.d - t.r0);
     t.block0 = t.r.lo / BN;
     t.n = range_blocks<BN>(t.r);
-    t.from = w.from;
-    t.to = uint32_t(min(uint64_t(t.n), w.from + (w.end - w.at)));
+    const uint32_t to = uint32_t(min(uint64_t(EXTRA + t.n), w.from + (w.end - w.at)));
+    t.count = to - w.from;
+    t.from = w.from > EXTRA ? w.from - EXTRA : 0;
+    t.to = to - EXTRA;  // (work_begin and work_next leave no part without blocks of its own)
     if (t.from == 0 && t.to == t.n) {
         t.c_first = t.c_last = cta;
     } else {
-        const uint64_t x0 = w.at - w.from;
+        const uint64_t x0 = w.at - w.from + EXTRA;
         t.c_first = work_owner(w, x0);
         t.c_last = work_owner(w, x0 + t.n - 1);
     }
@@ -234,10 +238,10 @@ __device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w, ui
 }
 
 // On to the next tile; false at the end of the share.
-template <int TR>
+template <int TR, int EXTRA>
 __device__ __forceinline__ bool work_next(const AttnParams &p, Work &w, const Part &t) {
-    w.at += t.to - t.from;
-    if (w.at >= w.end) return false;
+    w.at += t.count;
+    if (w.at + EXTRA >= w.end) return false;
     w.from = 0;
     if (++w.tile < seq_tiles<TR>(p, t.s)) return true;
     w.tile = 0;

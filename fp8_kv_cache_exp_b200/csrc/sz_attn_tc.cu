@@ -52,6 +52,9 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;
 constexpr int kTcBlock = 128;
+// A tile's fixed costs in blocks: 0, 1, 2, 3, 4 took 48.2, 45.9, 46.0, 46.0 and
+// 49.5 us for two 1024-token prompts of 32 heads of 80.
+constexpr int kTcExtra = 2;
 constexpr uint32_t kFewParts = 4;             // a tile of so many parts is joined by the last of them
 constexpr uint32_t kQPanel = 128 * 128;       // bytes of 128 rows of 64 16-bit elements
 constexpr uint32_t kPanel = kTcBlock * 128;   // of a block's rows
@@ -83,13 +86,12 @@ struct TcCfg {
 struct TcAux {
     uint64_t full[10], empty[10];
     uint64_t raw_full[8], raw_empty[8];
-    uint64_t q_full[2], q_empty[2], q_here[2];  // (q_here: E5M2, queries as they come)
+    uint64_t q_full[2], q_empty[2], q_here[2];  // (q_here: E5M2, queries as they come, for the softmax's threads to make fp16)
     uint64_t s_full[2], p_full[2][2];  // a tile's scores; the halves of its weights
     uint64_t o_full[2];                // a tile's sums, at the end of a part
     uint64_t turn[2];                  // a tile's turn at ex2
     uint64_t drain[2];
     uint32_t tmem, abort, bad;
-    int8_t exp[kTcRows];  // E5M2: exponent taken out of each query row
 };
 static_assert(sizeof(TcAux) <= 1024, "aux");
 
@@ -256,6 +258,17 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     return r;
 }
 
+// 32 bytes of a row, a whole sector, where its address allows it.
+__device__ __forceinline__ void store32(uint8_t *a, const uint32_t (&v)[8], bool aligned32) {
+    if (aligned32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(a)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(a)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 // ------------------------------------------------------------------- roles
 
 // Keys and values into shared memory (warps 8-11), in the order in which they
@@ -307,7 +320,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
             for (uint32_t i = 0; i < 1u << 16 && !mbar_try_wait(&bars[x % ring], (x / ring) & 1); ++i) {}
     };
     for (;;) {
-        const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
+        const Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
         const int32_t *ids = p.cache.table + uint64_t(w.seq) * p.cache.table_stride;
         const uint32_t part_hi = min((t.block0 + t.to) * kTcBlock, t.r.hi);
         const uint64_t head_off = uint64_t(w.head) * d * C::EB + piece * 16;
@@ -442,7 +455,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
                 }
                 raws += tiles;
             }
-            if (!work_next<kTcRows>(p, w, t)) return;
+            if (!work_next<kTcRows, kTcExtra>(p, w, t)) return;
             continue;
         }
         int32_t id = page_id(t.from);
@@ -474,13 +487,13 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
             hand_over(issued);
         } else {
             const uint32_t raw = base + C::RAW_AT + tid * 16;
-            for (uint32_t n = 0; n < tiles + C::RAWS - 1; ++n) {
+            constexpr uint32_t LAG = 2;  // tiles under way behind the one that is spread
+            for (uint32_t n = 0; n < tiles + LAG; ++n) {
                 if (n < tiles) next_copy(n, [&](uint32_t u) { return raw + (n % C::RAWS) * C::RAW + u * 2048; });
                 else cp_commit();
-                if (n + 1 < C::RAWS) continue;
-                const uint32_t m = n + 1 - C::RAWS;  // the tile that has come
-                if (m >= tiles) continue;
-                cp_wait<C::RAWS - 1>();
+                if (n < LAG) continue;
+                const uint32_t m = n - LAG;  // the tile that has come
+                cp_wait<LAG>();
                 if (!wait_free(issued)) return;
                 if (has_piece) {
 #pragma unroll
@@ -498,7 +511,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
             }
             cp_wait<0>();
         }
-        if (!work_next<kTcRows>(p, w, t)) return;
+        if (!work_next<kTcRows, kTcExtra>(p, w, t)) return;
     }
 }
 
@@ -513,37 +526,37 @@ __device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMa
     constexpr uint32_t BATCH = 8;
     const uint32_t lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 14, c = lane % QL;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i]; bit 2 + i: of q_here[i]
+    uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i]
     for (;;) {
-        const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
+        const Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
         const uint8_t *q = p.q.p + uint64_t(t.s.q0) * p.q.ts + uint64_t(w.head * G) * p.q.hs;
         for (uint32_t i = 0; i * 128 < t.rows; ++i) {
             if (seen & (1u << i)) {
                 if (!warp_wait(&aux->q_empty[i], (phases >> i) & 1, aux, p.ctl)) {
                     // giving up: tensor copies that are under way land, or a limit passes
-                    for (uint32_t x = 0; DT == SZ_BF16 && map && x < 2; ++x)
-                        for (uint32_t n = 0; (seen >> x & 1) && n < 1u << 16 && !mbar_try_wait(&aux->q_full[x], (phases >> x) & 1); ++n) {}
+                    uint64_t *here = DT == SZ_BF16 ? aux->q_full : aux->q_here;
+                    for (uint32_t x = 0; map && x < 2; ++x)
+                        for (uint32_t n = 0; (seen >> x & 1) && n < 1u << 16 && !mbar_try_wait(&here[x], (phases >> x) & 1); ++n) {}
                     return;
                 }
                 phases ^= 1u << i;
             }
             seen |= 1u << i;
             const uint32_t tile = base + i * C::QTILE + (c / 8) * kQPanel;
+            uint64_t *bar = DT == SZ_BF16 ? &aux->q_full[i] : &aux->q_here[i];
             if (map) {
-                uint64_t *bar = DT == SZ_BF16 ? &aux->q_full[i] : &aux->q_here[i];
                 if (warp == 0 && lane == 0) {
                     mbar_arrive_expect_tx(bar, C::QTILE);
                     const uint32_t token = t.s.q0 + div_by(t.r0 + i * 128, p.group);
                     for (uint32_t x = 0; x < C::PANELS; ++x)
                         tensor3_g2s(base + i * C::QTILE + x * kQPanel, map, x * 64, w.head * G, token, bar);
-                } else if (DT == SZ_BF16) {
+                } else {
                     bar_arrive(bar);
                 }
                 __syncwarp();
-                if constexpr (DT == SZ_BF16) continue;
-                if (!warp_wait(bar, (phases >> (2 + i)) & 1, aux, p.ctl)) return;
-                phases ^= 1u << (2 + i);
-            } else {
+                continue;
+            }
+            {
                 for (uint32_t r0 = warp * BATCH * QR; r0 < 128; r0 += kQueryWarps * BATCH * QR) {
                     // a lane finds one row; rows behind the last are zeros
                     const uint32_t mine = i * 128 + r0 + lane % (BATCH * QR);
@@ -567,35 +580,11 @@ __device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMa
             }
             cp_commit();
             cp_wait<0>();
-            if constexpr (DT == SZ_FP8_E5M2) {
-                // to fp16, behind the row's power of two, each lane what it copied
-                for (uint32_t r0 = warp * BATCH * QR; r0 < 128; r0 += kQueryWarps * BATCH * QR) {
-#pragma unroll
-                    for (uint32_t u = 0; u < BATCH; ++u) {
-                        const uint32_t r = r0 + u * QR + lane / QL;
-                        const uint32_t at = tile + r * 128 + (((c % 8) ^ (r & 7)) << 4);
-                        const uint4 v = c * 8 < d ? lds_u128(at) : make_uint4(0, 0, 0, 0);
-                        uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                        float top = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
-#pragma unroll
-                        for (int s = QL / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-                        int e = 0;
-                        if (top > 0.f && top < INFINITY) e = min(13 - (int(__float_as_uint(top) >> 23) - 127), 120);
-                        const float up = __uint_as_float(uint32_t(127 + e) << 23);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = pack_f16(bf16_lo(x[j]) * up, bf16_hi(x[j]) * up);
-                        if (c * 8 < d) sts_u128(at, make_uint4(x[0], x[1], x[2], x[3]));
-                        if (c == 0) aux->exp[i * 128 + r] = int8_t(e);
-                    }
-                }
-            }
             fence_proxy_async_smem();
-            bar_arrive(&aux->q_full[i]);
+            bar_arrive(bar);
             __syncwarp();
         }
-        if (!work_next<kTcRows>(p, w, t)) return;
+        if (!work_next<kTcRows, kTcExtra>(p, w, t)) return;
     }
 }
 
@@ -636,9 +625,15 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
         for (uint32_t k = half * 4; k < half * 4 + 4; ++k)
             mma_ts(256 + i * 128, i * 128 + k * 8, vd + k * (2048 >> 4), pv_desc, add || k > 0);
     };
+    Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
     for (;;) {
-        const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const uint32_t n = t.to - t.from;
+        Part after = t;  // the next part, found while the first scores are on their way
+        bool more = false;
+        auto look_ahead = [&]() {
+            more = work_next<kTcRows, kTcExtra>(p, w, t);
+            if (more) after = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
+        };
         if (i * 128 < t.rows) {
             if (!full(kv)) return;
             if (!wait(&aux->q_full[i], 2)) return;
@@ -649,6 +644,7 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
                 if (n == 1) tc_commit(&aux->q_empty[i]);
             }
             __syncwarp();
+            look_ahead();
             for (uint32_t j = 0; j < n; ++j) {
                 const uint32_t v = kv + 2 * j + 1, k = v + 1;
                 const uint64_t vd = stage(v), kd = stage(k);
@@ -676,6 +672,7 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
                 __syncwarp();
             }
         } else {
+            look_ahead();
             // the other tile's stages need this one's word too
             for (uint32_t j = 0; j < 2 * n; ++j) {
                 if (!full(kv + j)) return;
@@ -684,7 +681,8 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
             }
         }
         kv += 2 * n;
-        if (!work_next<kTcRows>(p, w, t)) return;
+        if (!more) return;
+        t = after;
     }
 }
 
@@ -719,6 +717,7 @@ __device__ __forceinline__ void join_few(const AttnParams &p, const Work &w, con
     const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * p.group.d + (g - tok * p.group.d);
     const float inv = L == 0.f ? 0.f : 1.f / L;
     uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs;
+    const bool aligned32 = ((reinterpret_cast<uintptr_t>(p.out.p) | p.out.ts | p.out.hs) & 31) == 0;
     float worst = 0.f;
     for (uint32_t e = 0; e < d; e += 16) {
         float v[16];
@@ -742,8 +741,7 @@ __device__ __forceinline__ void join_few(const AttnParams &p, const Work &w, con
             pk[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
         }
         if (r < t.rows) {
-            *reinterpret_cast<uint4 *>(out + 2 * e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            *reinterpret_cast<uint4 *>(out + 2 * e + 16) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            store32(out + 2 * e, pk, aligned32);
         }
     }
     if (r < t.rows) {
@@ -755,16 +753,23 @@ __device__ __forceinline__ void join_few(const AttnParams &p, const Work &w, con
 
 // Softmax of one tile's rows, a thread a row, and what becomes of the sums.
 template <int DT, int DP>
-__device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux *aux, TcDesc *desc) {
+__device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux, TcDesc *desc) {
     using C = TcCfg<DT, DP>;
     const uint32_t i = threadIdx.x / 128, row = threadIdx.x & 127;
     const uint32_t lanes = (threadIdx.x & 96) << 16;  // the warp's quarter of tensor memory
     const uint32_t s_at = lanes + i * 128, o_at = lanes + 256 + i * 128;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
     uint32_t q_uses = 0, s_uses = 0, o_uses = 0, turns = 0;
+    Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
     for (;;) {
-        const Part t = work_part<kTcRows, kTcBlock>(p, w, blockIdx.x);
         const bool whole_tile = t.c_first == t.c_last;
+        Work next = w;  // the part behind this one, found while this one's last product runs
+        Part after = t;
+        bool more = false;
+        auto look_ahead = [&]() {
+            more = work_next<kTcRows, kTcExtra>(p, next, t);
+            if (more) after = work_part<kTcRows, kTcBlock, kTcExtra>(p, next, blockIdx.x);
+        };
         const uint32_t parts = t.c_last - t.c_first + 1;
         if (threadIdx.x == 0 && parts > kFewParts && t.c_first == blockIdx.x) {
             desc->join = w;
@@ -777,12 +782,36 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
             // every row of the 128 sees [full_lo, full_hi)
             const uint32_t full_hi = token_range(p, t.s, div_by(t.r0 + i * 128, p.group)).hi;
             const uint32_t full_lo = token_range(p, t.s, div_by(t.r0 + min(i * 128 + 128, t.rows) - 1, p.group)).lo;
-            if (!warp_wait(&aux->q_full[i], q_uses++ & 1, aux, p.ctl)) return;
             float sc = p.scale_log2;
-            if constexpr (DT == SZ_FP8_E5M2) sc *= __uint_as_float(uint32_t(127 - aux->exp[r]) << 23);
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) bar_arrive(&aux->q_empty[i]);
-            __syncwarp();
+            if constexpr (DT == SZ_FP8_E5M2) {
+                // the row's queries to fp16, behind a power of two that its scores are divided by
+                if (!warp_wait(&aux->q_here[i], q_uses++ & 1, aux, p.ctl)) return;
+                const uint32_t at = base + i * C::QTILE + row * 128;
+                const auto chunk = [&](uint32_t c) { return at + (c / 8) * kQPanel + (((c % 8) ^ (row & 7)) << 4); };
+                uint32_t big = 0;  // of magnitudes as 16-bit integers, whose order is that of the numbers
+                for (uint32_t c = 0; c < d / 8; c += 2) {
+                    const uint4 u = lds_u128(chunk(c)), v = lds_u128(chunk(c + 1));
+                    const uint32_t y = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                                __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+                    const uint32_t z = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                    big = __vmaxu2(big, __vmaxu2(y, z));
+                }
+                big = max(big >> 16, big & 0xffffu);
+                // (no finite power for a row of zeros, or with infinities or NaN)
+                const int e = big > 0 && big < 0x7f80u ? min(13 - (int(big >> 7) - 127), 120) : 0;
+                const float up = __uint_as_float(uint32_t(127 + e) << 23);
+                for (uint32_t c = 0; c < d / 8; c += 2) {
+                    const uint4 u = lds_u128(chunk(c)), v = lds_u128(chunk(c + 1));
+                    sts_u128(chunk(c), make_uint4(pack_f16(bf16_lo(u.x) * up, bf16_hi(u.x) * up), pack_f16(bf16_lo(u.y) * up, bf16_hi(u.y) * up),
+                                                  pack_f16(bf16_lo(u.z) * up, bf16_hi(u.z) * up), pack_f16(bf16_lo(u.w) * up, bf16_hi(u.w) * up)));
+                    sts_u128(chunk(c + 1), make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                                                      pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up)));
+                }
+                sc *= __uint_as_float(uint32_t(127 - e) << 23);
+                fence_proxy_async_smem();
+                bar_arrive(&aux->q_full[i]);
+            }
             float m = -INFINITY, l = 0.f;
             for (uint32_t j = t.from; j < t.to; ++j) {
                 if (!warp_wait(&aux->s_full[i], s_uses++ & 1, aux, p.ctl)) return;
@@ -895,12 +924,14 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                 f2_split(f2_add(sum[0], sum[1]), a, b);
                 l += a + b;
             }
+            look_ahead();
             if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p.ctl)) return;
             tc_after();
             if (whole_tile) {
                 const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
                 const float f = l == 0.f ? 0.f : 1.f / l;
                 uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs;
+                const bool aligned32 = ((reinterpret_cast<uintptr_t>(p.out.p) | p.out.ts | p.out.hs) & 31) == 0;
                 float worst = 0.f;
                 for (uint32_t k = 0; k < d; k += 16) {
                     uint32_t o[16];
@@ -914,8 +945,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
                         pk[e] = pack_bf16(a, b);
                     }
                     if (r < t.rows) {
-                        *reinterpret_cast<uint4 *>(out + 2 * k) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                        *reinterpret_cast<uint4 *>(out + 2 * k + 16) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                        store32(out + 2 * k, pk, aligned32);
                     }
                 }
                 if (r < t.rows) {
@@ -943,8 +973,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, TcAux 
             }
             // the sums are read before the next part's first weights are announced
             tc_before();
+        } else {
+            look_ahead();
         }
-        if (!work_next<kTcRows>(p, w, t)) return;
+        if (!more) return;
+        w = next;
+        t = after;
     }
 }
 
@@ -971,9 +1005,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&aux->raw_empty[i], 128);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&aux->q_full[i], 32 * kQueryWarps);
-            mbar_init(&aux->q_here[i], 1);
-            mbar_init(&aux->q_empty[i], 1 + 4);  // the products, and the warps of the tile's softmax
+            mbar_init(&aux->q_full[i], DT == SZ_BF16 ? 32 * kQueryWarps : 128);
+            mbar_init(&aux->q_here[i], 32 * kQueryWarps);
+            mbar_init(&aux->q_empty[i], 1);
             mbar_init(&aux->s_full[i], 1);
             for (int h = 0; h < 2; ++h) mbar_init(&aux->p_full[i][h], 128);
             mbar_init(&aux->o_full[i], 1);
@@ -988,7 +1022,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
     Work w;
-    const bool has = work_begin<kTcThreads, kTcRows, kTcBlock>(
+    const bool has = work_begin<kTcThreads, kTcRows, kTcBlock, kTcExtra>(
         p, *reinterpret_cast<WorkScratch<kTcThreads> *>(smem + C::RING_AT), w);
     if (tid == 0) {
         desc->joins = 0;
@@ -1011,7 +1045,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 " SZ_TC_REGS_SOFTMAX ";");
-        softmax_role<DT, DP>(p, w, aux, desc);
+        softmax_role<DT, DP>(p, w, base, aux, desc);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " SZ_TC_REGS_OTHER ";");
         if (warp < 12) {
@@ -1078,7 +1112,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         while (nth >= s_list[k][0]) nth -= s_list[k++][0];
         const uint32_t c = s_list[k][1 + nth];
         const Work w = descs[c].join;
-        const Part t = work_part<kTcRows, kTcBlock>(p, w, c);
+        const Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, c);
         if (slice * kJoinRows < t.rows) {
             __syncthreads();  // (the last item's sums are read)
             const uint32_t r = slice * kJoinRows + lane, parts = t.c_last - t.c_first + 1;
@@ -1160,7 +1194,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         // rows that are not finite of the tiles that the CTA had alone, or joined
         Work w = descs[c].begin;
         for (;;) {
-            const Part t = work_part<kTcRows, kTcBlock>(p, w, c);
+            const Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, c);
             if (t.c_last - t.c_first < kFewParts)
                 for (uint32_t r = warp; r < t.rows; r += kJoinWarps) {
                     const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
@@ -1170,7 +1204,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
                     for (uint32_t e = lane; e < d; e += 32) bad = bad || (out[e] & 0x7f80u) == 0x7f80u;
                     if (__any_sync(0xffffffffu, bad)) repair_row<DT>(p, t.s, w.seq, w.head, g, t.r);
                 }
-            if (!work_next<kTcRows>(p, w, t)) break;
+            if (!work_next<kTcRows, kTcExtra>(p, w, t)) break;
         }
     }
 }
