@@ -176,6 +176,7 @@ sz_status sz_kv_append_paged(const sz_kv_cache_t *cache, const sz_kv_append_t *a
     rope_params(p, a->norm, a->rope);
     p.tokens = uint32_t(a->tokens);
     p.head_dim = dim;
+    p.inv_dim = 1.f / float(dim);
     const int sms = num_sms();
     if (sms <= 0) return SZ_ERR_CUDA;
     return launch_rope(p, true, int(cache->dtype), sms, stream);
@@ -212,6 +213,7 @@ sz_status sz_qk_norm_rope(const sz_qk_norm_rope_t *a, void *d_ws, size_t ws_byte
     rope_params(p, a->norm, a->rope);
     p.tokens = uint32_t(a->tokens);
     p.head_dim = dim;
+    p.inv_dim = 1.f / float(dim);
     const int sms = num_sms();
     if (sms <= 0) return SZ_ERR_CUDA;
     return launch_rope(p, false, SZ_BF16, sms, stream);

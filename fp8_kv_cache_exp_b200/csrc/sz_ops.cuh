@@ -54,7 +54,7 @@ struct RopeParams {
     HeadsRef q, q_out, k, k_out, v;
     const int32_t *cu_q, *kv_len;
     const uint8_t *q_weight, *k_weight;
-    float eps;
+    float eps, inv_dim;  // (1 / head_dim)
     RopeRef rope;
     uint32_t tokens, head_dim;
     FastDiv chunks;  // chunks of heads to a token
