@@ -4,11 +4,10 @@ KV-cache tensors on a B200 GPU (SplitZip project page, Abstract and FAQ).
 Argument marshalling only: the functions below have the names of the C ABI in
 include/splitzip.h and pass torch tensors' device pointers and the current CUDA
 stream to it.  Every step of the codec runs in the library's CUDA kernels.
-Importing this package loads libsplitzip.so and raises ImportError if it has not
-been built (python fp8_kv_cache_exp_b200/build.py); there is no other path.
+Importing this package loads libsplitzip.so and _host.so and raises ImportError if they
+have not been built (python fp8_kv_cache_exp_b200/build.py); there is no other path.
 """
 import ctypes
-import math
 import os
 import struct
 
@@ -102,6 +101,24 @@ def _load():
 
 
 lib = _load()
+
+
+def _load_host():
+    path = os.path.join(os.path.dirname(lib_path), "_host.so")
+    if not os.path.exists(path):
+        raise ImportError("_host.so is not built (%s); run: python fp8_kv_cache_exp_b200/build.py" % path)
+    from importlib.machinery import ExtensionFileLoader
+    from importlib.util import module_from_spec, spec_from_loader
+    loader = ExtensionFileLoader(__name__ + "._host", path)
+    host = module_from_spec(spec_from_loader(loader.name, loader))
+    loader.exec_module(host)
+    entries = (lib.sz_kv_append_paged, lib.sz_qk_norm_rope, lib.sz_attn_paged)
+    if host.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries)) != 0:
+        raise ImportError("libsplitzip.so lacks the operators' entry points")
+    return host
+
+
+_host = _load_host()
 
 
 class SplitZipError(RuntimeError):
@@ -465,15 +482,10 @@ def sz_encode_noalloc(dtype: int, plan: torch.Tensor, x: torch.Tensor, out: torc
 
 # ------------------------------------------------ operators on a paged cache
 #
-# The argument structs of include/splitzip.h are packed by `struct` with native
-# alignment and handed over as bytes: one call's structs belong to that call
-# alone, so calls from several threads do not share them.
+# Their arguments are checked and packed by the module _host (csrc/sz_host.cpp):
+# once for each layer and token, that has to be quick.
 
 _CACHE = struct.Struct("@3Q2Q8I")                         # sz_kv_cache_t
-_APPEND = struct.Struct("@Q" + "3Q2I" * 4 + "2Q" + "2QfI" + "2Q4I")   # sz_kv_append_t
-_NORM_ROPE = struct.Struct("@Q" + "3Q2I" * 4 + "2QfI" + "2Q4I" + "2I")  # sz_qk_norm_rope_t
-_ATTN = struct.Struct("@Q" + "3Q2I" * 2 + "3Q" + "f3I")   # sz_attn_t
-_NO_HEADS = (0, 0, 0, 0, 0)
 
 
 class KVCache:
@@ -548,55 +560,6 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, device="cuda") -
     return torch.cat([a.cos(), a.sin()], 1).float()
 
 
-def _on(dev: int, *tensors):
-    """Every tensor is on CUDA device `dev`, and that is the current device."""
-    for x in tensors:
-        if x is not None and x.get_device() != dev:
-            raise ValueError("all tensors must be on the cache's device (the first tensor's)")
-    if dev < 0 or torch.cuda.current_device() != dev:
-        raise ValueError("the tensors' CUDA device must be the current device")
-
-
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _heads(x: torch.Tensor, dim: int, name: str):
-    """sz_heads_t of a bfloat16 view [tokens, heads, dim] whose rows are contiguous."""
-    if x.dtype != torch.bfloat16:
-        raise TypeError("%s: bfloat16" % name)
-    shape = x.shape
-    if len(shape) != 3 or shape[2] != dim:
-        raise ValueError("%s: [tokens, heads, %d]" % (name, dim))
-    ts, hs, es = x.stride()
-    if es != 1:
-        raise ValueError("%s: a head's elements must be contiguous" % name)
-    return x.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0, shape[1], 0
-
-
-def _vector(x, dtype, n, name):
-    """Device pointer of a contiguous vector of n elements (0 for None)."""
-    if x is None:
-        return 0
-    if x.dtype != dtype:
-        raise TypeError("%s: %s" % (name, dtype))
-    if x.numel() != n or not x.is_contiguous():
-        raise ValueError("%s: %d contiguous elements" % (name, n))
-    return x.data_ptr()
-
-
-def _norm_rope_args(dim, tokens, q_norm, k_norm, eps, rope, positions, interleaved):
-    norm = (_vector(q_norm, torch.bfloat16, dim, "q_norm"), _vector(k_norm, torch.bfloat16, dim, "k_norm"),
-            eps, 0)
-    if rope is None:
-        return norm + (0, 0, 0, 0, 0, 0)
-    if rope.dim() != 2:
-        raise ValueError("rope: [positions, rot]")
-    n, rot = rope.shape
-    return norm + (_vector(rope, torch.float32, n * rot, "rope"),
-                   _vector(positions, torch.int32, tokens, "positions"), n, rot, 1 if interleaved else 0, 0)
-
-
 def sz_kv_append_paged(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor,
                        ws: torch.Tensor, q: torch.Tensor = None, q_out: torch.Tensor = None,
                        q_norm: torch.Tensor = None, k_norm: torch.Tensor = None, eps: float = 1e-6,
@@ -609,24 +572,8 @@ def sz_kv_append_paged(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_q: t
     cu_q[s]:cu_q[s+1] are the last tokens of sequence s, whose length with them is kv_len[s] (int32 device
     tensors); rows behind cu_q[-1] are left alone.  q_norm, k_norm: bfloat16 [head_dim]; rope: float32
     [positions, rot], see rope_table; positions: int32 [tokens], default each token's place."""
-    dim, tokens = cache.head_dim, k.shape[0]
-    _on(cache._dev, k, v, cu_q, kv_len, ws, q, q_out, q_norm, k_norm, rope, positions)
-    if v.shape[0] != tokens or (q is not None and q.shape[0] != tokens):
-        raise ValueError("k, v and q must have the same number of tokens")
-    qh = oh = _NO_HEADS
-    if q is not None:
-        qh = _heads(q, dim, "q")
-        oh = qh if q_out is None else _heads(q_out, dim, "q_out")
-        if q_out is not None and q_out.shape[0] != tokens:
-            raise ValueError("q_out must have q's shape")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    args = _APPEND.pack(tokens, *_heads(k, dim, "k"), *_heads(v, dim, "v"), *qh, *oh,
-                        _vector(cu_q, torch.int32, cache.seqs + 1, "cu_q"),
-                        _vector(kv_len, torch.int32, cache.seqs, "kv_len"),
-                        *_norm_rope_args(dim, tokens, q_norm, k_norm, eps, rope, positions, interleaved))
-    _check(lib.sz_kv_append_paged(cache._c, args, _ptr(ws), ws.nbytes, _raw_stream(stream, cache._dev)),
-           "sz_kv_append_paged")
+    _check(_host.append(cache._c, cache._dev, k, v, cu_q, kv_len, ws, q, q_out, q_norm, k_norm, eps, rope, positions,
+                        interleaved, None if stream is None else stream.cuda_stream), "sz_kv_append_paged")
 
 
 def sz_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_out: torch.Tensor, k_out: torch.Tensor, ws: torch.Tensor,
@@ -635,24 +582,8 @@ def sz_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_out: torch.Tensor, k_out
                     stream=None):
     """Normalise and rotate query and key heads [tokens, heads, head_dim] (bfloat16 views; q or k may be
     None with its output).  Outputs may be the inputs themselves.  positions: int32 [tokens]."""
-    x = q if q is not None else k
-    if x is None:
-        raise ValueError("q or k")
-    tokens, dim = x.shape[0], x.shape[-1]
-    _on(x.get_device(), q, k, q_out, k_out, ws, q_norm, k_norm, rope, positions)
-    views = []
-    for a, b, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if (a is None) != (b is None):
-            raise ValueError("%s and %s_out come together" % (name, name))
-        if a is None:
-            views += _NO_HEADS + _NO_HEADS
-            continue
-        if a.shape[0] != tokens or b.shape[0] != tokens:
-            raise ValueError("q, k and their outputs must have the same number of tokens")
-        views += _heads(a, dim, name) + _heads(b, dim, name + "_out")
-    args = _NORM_ROPE.pack(tokens, *views,
-                           *_norm_rope_args(dim, tokens, q_norm, k_norm, eps, rope, positions, interleaved), dim, 0)
-    _check(lib.sz_qk_norm_rope(args, _ptr(ws), ws.nbytes, _raw_stream(stream, x.get_device())), "sz_qk_norm_rope")
+    _check(_host.norm_rope(q, k, q_out, k_out, ws, q_norm, k_norm, eps, rope, positions, interleaved,
+                           None if stream is None else stream.cuda_stream), "sz_qk_norm_rope")
 
 
 def sz_attn_paged(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, out: torch.Tensor,
@@ -662,13 +593,5 @@ def sz_attn_paged(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len: t
     [tokens, heads, head_dim] (bfloat16 views) of the sequences that cu_q and kv_len describe (as in
     sz_kv_append_paged; the tokens' own keys and values are in the cache).  scale: default head_dim^-0.5;
     window: w > 0 lets a row see the last w places up to its own; lse: float32 [tokens, heads]."""
-    dim, tokens = cache.head_dim, q.shape[0]
-    _on(cache._dev, q, cu_q, kv_len, out, ws, lse)
-    if out.shape[0] != tokens:
-        raise ValueError("out must have q's shape")
-    qh = _heads(q, dim, "q")
-    args = _ATTN.pack(tokens, *qh, *_heads(out, dim, "out"), _vector(cu_q, torch.int32, cache.seqs + 1, "cu_q"),
-                      _vector(kv_len, torch.int32, cache.seqs, "kv_len"),
-                      _vector(lse, torch.float32, tokens * qh[3], "lse"),
-                      1.0 / math.sqrt(dim) if scale is None else scale, 1 if causal else 0, window, 0)
-    _check(lib.sz_attn_paged(cache._c, args, _ptr(ws), ws.nbytes, _raw_stream(stream, cache._dev)), "sz_attn_paged")
+    _check(_host.attn(cache._c, cache._dev, q, cu_q, kv_len, out, ws, cache.head_dim ** -0.5 if scale is None else scale,
+                      causal, window, lse, None if stream is None else stream.cuda_stream), "sz_attn_paged")

@@ -1,10 +1,12 @@
-"""Build libsplitzip.so (the CUDA library behind the C ABI) in-tree for sm_100a.
+"""Build libsplitzip.so (the CUDA library behind the C ABI) in-tree for sm_100a,
+and _host (the Python binding's argument checks of the paged-cache operators).
 
 Usage: python fp8_kv_cache_exp_b200/build.py [--force]
 (run it by path: importing the package itself loads the library it builds)
 """
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
@@ -13,6 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsplitzip.so")
+HOST = os.path.join(HERE, "_host.so")
+HOST_SRC = os.path.join(CSRC, "sz_host.cpp")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -39,9 +43,39 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def host_up_to_date() -> bool:
+    return os.path.exists(HOST) and all(os.path.getmtime(p) <= os.path.getmtime(HOST)
+                                        for p in (HOST_SRC, os.path.join(INCLUDE, "splitzip.h")))
+
+
+def build_host(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/sz_host.cpp against this interpreter and its torch."""
+    if not force and host_up_to_date():
+        return HOST
+    import sysconfig
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(os.environ.get("NVCC", "nvcc")) or
+                                                            "/usr/local/cuda/bin/nvcc")))
+    tmp = HOST + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(at, "include"),
+           "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-o", tmp, HOST_SRC,
+           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, HOST)
+    return HOST
+
+
 def build(force: bool = False, extra_flags=(), out: str = LIB, verbose: bool = False) -> str:
     """Compile every csrc/*.cu (one nvcc per file, in parallel) and link them
     into one shared library; return its path."""
+    if out == LIB:
+        build_host(force, verbose)
     if not force and out == LIB and up_to_date():
         return out
     import tempfile
