@@ -26,6 +26,12 @@ constexpr int kPlaces = 16;  // places of a warp's step
 constexpr int kSplitBlock = 64;
 constexpr int kSplitExtra = 0;
 
+// Parts of a tile that a CTA joins at a time: up to kJoinMost at once, more of
+// them in groups first.
+constexpr int kJoinMost = 32;
+__device__ __forceinline__ uint32_t join_group(uint32_t parts) { return parts <= 16 ? parts : (parts <= 144 ? 12 : 24); }
+static_assert(kAttnCtas <= 24 * kJoinMost, "groups");
+
 template <int DT, int DP, int MT>
 struct SplitCfg {
     static constexpr int EB = DT == SZ_BF16 ? 2 : 1;
@@ -37,7 +43,7 @@ struct SplitCfg {
     static constexpr int QPITCH = DP * 2 + 16;
     static constexpr int OPITCH = DP + 4;                  // floats
     static constexpr int JOIN = kSplitWarps * TR * OPITCH * 4;
-    static constexpr int WEIGHTS = int(kAttnCtas) * TR * 4;
+    static constexpr int WEIGHTS = kJoinMost * TR * 4;
     static constexpr int MAIN = RING > JOIN ? (RING > WEIGHTS ? RING : WEIGHTS) : (JOIN > WEIGHTS ? JOIN : WEIGHTS);
     static constexpr int SMEM = MAIN + TR * QPITCH;
     // what the softmax's powers are multiplied by: small ones keep their bits in fp16
@@ -411,47 +417,67 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
         }
         bool written = whole_tile;
         if (!whole_tile) {
-            const uint32_t parts = t.c_last - t.c_first + 1;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(&p.arrived[t.c_first], 1u) == parts - 1;
-            __syncthreads();
-            written = s_last != 0;
-            if (written) {
+            // Parts are joined by whoever comes last to them: of up to 16 at once, of more in
+            // groups, and then the groups; one CTA that reads 111 parts takes 30 us.
+            const uint32_t parts = t.c_last - t.c_first + 1, group = join_group(parts), mine = (blockIdx.x - t.c_first) / group;
+            const uint32_t groups = (parts + group - 1) / group;
+            // Whether this CTA is the last of n at a counter, which is then zero again.
+            auto last_of = [&](uint32_t *counter, uint32_t n) {
                 __threadfence();
-                // each part's factor for each row, then the sums
+                __syncthreads();
+                if (tid == 0) {
+                    s_last = atomicAdd(counter, 1u) == n - 1;
+                    if (s_last) *counter = 0;
+                }
+                __syncthreads();
+                __threadfence();
+                return s_last != 0;
+            };
+            auto slot_of = [&](uint32_t k) { return p.part + uint64_t(part_slot(t.c_first + k, t)) * TR * (d + 2); };
+            // Joins parts first, first + step, ... (n of them) to the result, or to the first one's place.
+            auto join = [&](uint32_t first, uint32_t step, uint32_t n, bool result) {
                 float *s_f = reinterpret_cast<float *>(smem);
-                const float *base = p.part;
-                auto slot_of = [&](uint32_t k) { return uint64_t(part_slot(t.c_first + k, t)) * TR * (d + 2); };
                 for (uint32_t r = warp; r < t.rows; r += kSplitWarps) {
-                    float M = -INFINITY, L = 0.f;
-                    for (uint32_t k = lane; k < parts; k += 32) M = fmaxf(M, __ldcg(base + slot_of(k) + TR * d + r));
+                    const float *at = slot_of(first + min(lane, n - 1) * step) + TR * d + r;
+                    const float m = lane < n ? __ldcg(at) : -INFINITY;
+                    float M = m;
 #pragma unroll
                     for (int v = 16; v > 0; v >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, v));
-                    const float safe = M == -INFINITY ? 0.f : M;
-                    for (uint32_t k = lane; k < parts; k += 32) {
-                        const float f = exp2_fast(__ldcg(base + slot_of(k) + TR * d + r) - safe);
-                        s_f[k * TR + r] = f;
-                        L += f * __ldcg(base + slot_of(k) + TR * d + TR + r);
-                    }
+                    const float f = lane < n ? exp2_fast(m - (M == -INFINITY ? 0.f : M)) : 0.f;
+                    float L = lane < n ? f * __ldcg(at + TR) : 0.f;
+                    s_f[lane * TR + r] = f;
 #pragma unroll
                     for (int v = 16; v > 0; v >>= 1) L += __shfl_xor_sync(0xffffffffu, L, v);
                     if (lane == 0) s_M[r] = M, s_L[r] = L;
                 }
                 __syncthreads();
+                float *to = slot_of(first);
                 for (uint32_t e = tid; e < t.rows * quads; e += kSplitThreads) {
                     const uint32_t r = e / quads, c = e - r * quads;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (uint32_t k = 0; k < parts; ++k) {
+#pragma unroll 12
+                    for (uint32_t k = 0; k < n; ++k) {
                         const float f = s_f[k * TR + r];
-                        const float4 a = __ldcg(reinterpret_cast<const float4 *>(base + slot_of(k) + r * d + c * 4));
+                        const float4 a = __ldcg(reinterpret_cast<const float4 *>(slot_of(first + k * step) + r * d + c * 4));
                         v.x = fmaf(f, a.x, v.x), v.y = fmaf(f, a.y, v.y);
                         v.z = fmaf(f, a.z, v.z), v.w = fmaf(f, a.w, v.w);
                     }
-                    finish(r, c, v, s_M[r], s_L[r]);
+                    if (result) {
+                        finish(r, c, v, s_M[r], s_L[r]);
+                    } else {
+                        *reinterpret_cast<float4 *>(to + r * d + c * 4) = v;
+                        if (c == 0) to[TR * d + r] = s_M[r], to[TR * d + TR + r] = s_L[r];
+                    }
                 }
-                if (tid == 0) p.arrived[t.c_first] = 0;
+            };
+            uint32_t *counter = mine == 0 ? p.arrived + t.c_first : p.arrived + kAttnCtas + t.c_first + mine * group;
+            if (last_of(counter, min(group, parts - mine * group))) {
+                join(mine * group, 1, min(group, parts - mine * group), groups == 1);
+                written = groups == 1;
+                if (groups > 1 && last_of(p.arrived + 2 * kAttnCtas + t.c_first, groups)) {
+                    join(0, group, groups, true);
+                    written = true;
+                }
             }
         }
         __syncthreads();

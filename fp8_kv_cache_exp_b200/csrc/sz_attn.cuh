@@ -123,9 +123,71 @@ __device__ __forceinline__ uint64_t block_scan64(uint64_t v, uint64_t *s_warp, u
     return before + x - v;
 }
 
+// The share of CTA blockIdx.x of `per_head` blocks a head, up to the tile that it begins in.
+__device__ __forceinline__ uint64_t work_share(const AttnParams &p, uint64_t per_head, Work &w) {
+    const uint64_t total = per_head * p.cache.kv_heads;
+    w.each = quotient(total, gridDim.x);
+    w.more = uint32_t(total - w.each * gridDim.x);
+    w.at = w.each * blockIdx.x + min(blockIdx.x, w.more);
+    w.end = w.at + w.each + (blockIdx.x < w.more ? 1 : 0);
+    w.head = per_head ? uint32_t(quotient(w.at, per_head)) : 0;
+    return w.at - w.head * per_head;
+}
+
+// The same for at most 32 sequences with at most 32 tiles together, each warp by
+// itself: the block's way (below) costs a call of one token 2 us.  Says whether
+// it was possible; then `has` is whether the CTA has a share.
+template <int TR, int BN, int EXTRA>
+__device__ __forceinline__ bool work_begin_few(const AttnParams &p, Work &w, bool &has) {
+    const uint32_t lane = threadIdx.x & 31, seqs = p.cache.seqs;
+    if (seqs > 32) return false;
+    SeqInfo si{0, 0, 0};
+    if (lane < seqs) {
+        si = seq_info(p, lane);
+        if (blockIdx.x == 0 && threadIdx.x < 32 && __ldg(p.kv_len + lane) > int32_t(p.cache.capacity))
+            set_error(p.ctl, SZ_ERR_INVALID_ARG, lane);
+    }
+    const uint32_t tiles = seq_tiles<TR>(p, si);
+    if (__any_sync(0xffffffffu, tiles > 32)) return false;
+    uint32_t ends = tiles;  // of this lane's sequence's tiles
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, ends, o);
+        if (lane >= o) ends += y;
+    }
+    const uint32_t count = __shfl_sync(0xffffffffu, ends, 31);
+    if (count > 32) return false;
+    uint32_t seq = 0;  // of tile `lane`: the number of sequences that end at or before it
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1)
+        if (__shfl_sync(0xffffffffu, ends, int(seq + step - 1)) <= lane) seq += step;
+    seq = min(seq, 31u);
+    const uint32_t q_len = __shfl_sync(0xffffffffu, si.q_len, int(seq)), kv = __shfl_sync(0xffffffffu, si.kv, int(seq));
+    const uint32_t tile = lane - __shfl_sync(0xffffffffu, ends - tiles, int(seq));
+    const uint32_t units =
+        lane < count ? EXTRA + range_blocks<BN>(tile_range<TR>(p, SeqInfo{0, q_len, kv}, tile)) : 0;
+    uint64_t to = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, to, o);
+        if (lane >= o) to += y;
+    }
+    const uint64_t target = work_share(p, __shfl_sync(0xffffffffu, to, 31), w);
+    has = w.at < w.end;
+    if (!has) return true;
+    const int src = __ffs(__ballot_sync(0xffffffffu, target < to && target >= to - units)) - 1;
+    w.seq = __shfl_sync(0xffffffffu, seq, src);
+    w.tile = __shfl_sync(0xffffffffu, tile, src);
+    w.from = uint32_t(target - __shfl_sync(0xffffffffu, to - units, src));
+    has = w.from + (w.end - w.at) > EXTRA;
+    return true;
+}
+
 // The CTA's share; false if it has none.  All NT threads call it.
 template <int NT, int TR, int BN, int EXTRA>
 __device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w) {
+    bool has;
+    if (work_begin_few<TR, BN, EXTRA>(p, w, has)) return has;
     const uint32_t tid = threadIdx.x, seqs = p.cache.seqs;
     // this thread's tile of the chunk looked at last
     uint32_t seq = 0, tile = 0, units = 0, chunks = 0;
@@ -178,14 +240,8 @@ __device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w) {
         return run;
     };
     const uint64_t per_head = scan(false, 0);
-    const uint64_t total = per_head * p.cache.kv_heads;
-    w.each = quotient(total, gridDim.x);
-    w.more = uint32_t(total - w.each * gridDim.x);
-    w.at = w.each * blockIdx.x + min(blockIdx.x, w.more);
-    w.end = w.at + w.each + (blockIdx.x < w.more ? 1 : 0);
+    const uint64_t target = work_share(p, per_head, w);
     if (w.at == w.end) return false;
-    w.head = uint32_t(quotient(w.at, per_head));
-    const uint64_t target = w.at - w.head * per_head;
     if (chunks == 1) note(target);  // the one chunk is still at hand
     else scan(true, target);
     __syncthreads();

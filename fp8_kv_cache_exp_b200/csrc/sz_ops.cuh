@@ -140,8 +140,9 @@ sz_status launch_attn_tc(const AttnParams &p, int dtype, int num_sms, cudaStream
 // sums in float and two statistics a row.
 constexpr uint32_t kMaxSms = 160;
 constexpr uint32_t kAttnCtas = 3 * kMaxSms;  // most CTAs of any attention kernel
-constexpr size_t kArrivedBytes = size_t(kMaxSms) * 8 * 4;  // the tensor-memory kernel counts for each warp of a tile
-static_assert(kAttnCtas <= kMaxSms * 8, "arrival counters");
+// counters: three for each CTA of the split kernel, or one for each warp of a tile
+constexpr size_t kArrivedBytes = size_t(3) * kAttnCtas * 4;
+static_assert(kMaxSms * 8 <= 3 * kAttnCtas, "arrival counters");
 constexpr size_t kDescBytes = size_t(kMaxSms) * 128;
 // floats of all partials: the largest (CTAs * rows) of the kernels is a
 // persistent CTA for each SM with 256 rows, or kAttnCtas of 32
