@@ -23,6 +23,7 @@ namespace {
 constexpr int kSplitThreads = 128;
 constexpr int kSplitWarps = kSplitThreads / 32;
 constexpr int kPlaces = 16;  // places of a warp's step
+constexpr int kAhead = 4;
 constexpr int kSplitBlock = 64;
 constexpr int kSplitExtra = 0;
 
@@ -38,7 +39,11 @@ struct SplitCfg {
     static constexpr int TR = 16 * MT;
     static constexpr int PITCH = DP * EB + 16;             // odd in 16-byte units: rows fall on different banks
     static constexpr int STAGE = 2 * kPlaces * PITCH;      // keys, then values
-    static constexpr int STAGES = DP > 128 ? 2 : (DT == SZ_BF16 ? (DP > 64 ? 3 : 5) : (DP > 64 ? 5 : 8));
+    #ifndef SZ_SB
+#define SZ_SB 3
+#define SZ_SE 3
+#endif
+    static constexpr int STAGES = DP > 128 ? 2 : (DT == SZ_BF16 ? (DP > 64 ? SZ_SB : 5) : (DP > 64 ? SZ_SE : 5));
     static constexpr int RING = kSplitWarps * STAGES * STAGE;
     static constexpr int QPITCH = DP * 2 + 16;
     static constexpr int OPITCH = DP + 4;                  // floats
@@ -47,7 +52,9 @@ struct SplitCfg {
     static constexpr int MAIN = RING > JOIN ? (RING > WEIGHTS ? RING : WEIGHTS) : (JOIN > WEIGHTS ? JOIN : WEIGHTS);
     static constexpr int SMEM = MAIN + TR * QPITCH;
     // what the softmax's powers are multiplied by: small ones keep their bits in fp16
-    static constexpr float RAISE = DT == SZ_BF16 ? 0.f : 12.f;
+    static constexpr float RAISE = DT == SZ_BF16 ? 0.f : 8.f;
+    // how far a row's largest score may grow, as a power of two, before its sums are rescaled
+    static constexpr float SLACK = DT == SZ_BF16 ? 8.f : 6.f;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
@@ -121,11 +128,22 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
         const uint32_t steps = part_hi > part_lo ? (part_hi - part_lo + kPlaces - 1) / kPlaces : 0;
         const uint64_t head_off = uint64_t(w.head) * d * C::EB + piece * 16;
 
-        // page offset of the place that lane & 15 has in a step
-        auto lookup = [&](uint32_t step) -> uint64_t {
+        // The page id of the place that lane & 15 has in a step (-1: no place), and its offset.
+        // Ids are asked for kAhead steps before their offsets are needed: a step that waited
+        // for its own would take the load's latency.
+        auto page_id = [&](uint32_t step) -> int32_t {
+            const uint32_t at = part_lo + step * kPlaces + (lane & 15);
+            return step < steps && at >= t.r.lo && at < part_hi ? __ldg(ids + div_by(at, p.cache.page_tokens)) : -1;
+        };
+        auto offset = [&](uint32_t step, int32_t id) -> uint64_t {
             const uint32_t at = part_lo + step * kPlaces + (lane & 15);
             if (step >= steps || at < t.r.lo || at >= part_hi) return kBadOffset;
-            return place_offset(p.cache, p.ctl, ids, at);
+            const uint32_t page = div_by(at, p.cache.page_tokens);
+            if (id < 0 || uint64_t(id) >= p.cache.pool_pages) {
+                set_error(p.ctl, SZ_ERR_INVALID_ARG, page);
+                return kBadOffset;
+            }
+            return uint64_t(id) * p.cache.page_bytes + uint64_t(at - page * p.cache.page_tokens.d) * p.cache.row_bytes;
         };
         auto issue = [&](uint32_t slot, uint64_t off) {
             const uint32_t dst = ring + slot * C::STAGE + row0 * C::PITCH + piece * 16;
@@ -141,12 +159,19 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
         };
 
         // fill the ring
-        uint64_t off = lookup(warp);
+        int32_t id[kAhead];
+        {
+            int32_t first[C::STAGES - 1];
 #pragma unroll
-        for (int i = 0; i < C::STAGES - 1; ++i) {
-            if (warp + i * kSplitWarps < steps) issue(i, off);
-            cp_commit();
-            off = lookup(warp + (i + 1) * kSplitWarps);
+            for (int i = 0; i < C::STAGES - 1; ++i) first[i] = page_id(warp + i * kSplitWarps);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) id[i] = page_id(warp + (C::STAGES - 1 + i) * kSplitWarps);
+#pragma unroll
+            for (int i = 0; i < C::STAGES - 1; ++i) {
+                const uint32_t step = warp + i * kSplitWarps;
+                if (step < steps) issue(i, offset(step, first[i]));
+                cp_commit();
+            }
         }
 
         // queries of the tile's rows; rows behind the last are zeros
@@ -213,9 +238,11 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
             {
                 const uint32_t ahead = step + (C::STAGES - 1) * kSplitWarps;
                 const uint32_t to = slot == 0 ? C::STAGES - 1 : slot - 1;
-                if (ahead < steps) issue(to, off);
+                if (ahead < steps) issue(to, offset(ahead, id[0]));
                 cp_commit();
-                off = lookup(ahead + kSplitWarps);
+#pragma unroll
+                for (int i = 1; i < kAhead; ++i) id[i - 1] = id[i];
+                id[kAhead - 1] = page_id(ahead + kAhead * kSplitWarps);
             }
             cp_wait<C::STAGES - 1>();
             __syncwarp();
@@ -269,6 +296,10 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
             for (int i = 0; i < MT; ++i) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && t.rows <= 8u + 16u * i) {  // no rows there
+                        pa[i][1] = pa[i][3] = 0;
+                        continue;
+                    }
                     float e[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -281,18 +312,17 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
                     float top = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float mn = fmaxf(m[i][h], top);
-                    const float safe = mn == -INFINITY ? 0.f : mn;
-                    const float c = exp2_fast(m[i][h] - safe);
-                    if (__any_sync(0xffffffffu, mn != m[i][h])) {
+                    const bool grows = top > m[i][h] + C::SLACK;
+                    float c = 1.f;
+                    if (__any_sync(0xffffffffu, grows)) {
+                        if (grows) c = exp2_fast(m[i][h] - top), m[i][h] = top;
 #pragma unroll
                         for (int n = 0; n < DP / 8; ++n) {
                             o[i][n][h * 2] *= c;
                             o[i][n][h * 2 + 1] *= c;
                         }
                     }
-                    m[i][h] = mn;
-                    const float base = C::RAISE - safe;
+                    const float base = C::RAISE - (m[i][h] == -INFINITY ? 0.f : m[i][h]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) e[j] = exp2_fast(e[j] + base);
                     l[i][h] = l[i][h] * c + ((e[0] + e[1]) + (e[2] + e[3]));
