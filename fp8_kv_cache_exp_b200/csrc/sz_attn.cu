@@ -39,11 +39,7 @@ struct SplitCfg {
     static constexpr int TR = 16 * MT;
     static constexpr int PITCH = DP * EB + 16;             // odd in 16-byte units: rows fall on different banks
     static constexpr int STAGE = 2 * kPlaces * PITCH;      // keys, then values
-    #ifndef SZ_SB
-#define SZ_SB 3
-#define SZ_SE 3
-#endif
-    static constexpr int STAGES = DP > 128 ? 2 : (DT == SZ_BF16 ? (DP > 64 ? SZ_SB : 5) : (DP > 64 ? SZ_SE : 5));
+        static constexpr int STAGES = DP > 128 ? 2 : (DP > 64 ? 3 : 5);
     static constexpr int RING = kSplitWarps * STAGES * STAGE;
     static constexpr int QPITCH = DP * 2 + 16;
     static constexpr int OPITCH = DP + 4;                  // floats
@@ -116,6 +112,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
     constexpr uint32_t ROWS = 32 / LPR;
     const uint32_t piece = lane % LPR, row0 = lane / LPR;
     const bool has_piece = piece * 16 < d * C::EB;
+    const bool one_page = p.cache.page_tokens.d % kPlaces == 0;  // a step lies in one page
 
     Work w;
     if (!work_begin<kSplitThreads, TR, kSplitBlock, kSplitExtra>(p, s_work, w)) return;
@@ -132,6 +129,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
         // Ids are asked for kAhead steps before their offsets are needed: a step that waited
         // for its own would take the load's latency.
         auto page_id = [&](uint32_t step) -> int32_t {
+            if (one_page) return step < steps ? __ldg(ids + div_by(part_lo + step * kPlaces, p.cache.page_tokens)) : -1;
             const uint32_t at = part_lo + step * kPlaces + (lane & 15);
             return step < steps && at >= t.r.lo && at < part_hi ? __ldg(ids + div_by(at, p.cache.page_tokens)) : -1;
         };
@@ -159,6 +157,25 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
         };
 
         // fill the ring
+        // a step's copies: without a look at each place where all are seen and in one page
+        auto issue_step = [&](uint32_t slot, uint32_t step, int32_t id) {
+            const uint32_t at = part_lo + step * kPlaces;
+            if (one_page && at >= t.r.lo && at + kPlaces <= part_hi && id >= 0 && uint64_t(id) < p.cache.pool_pages) {
+                const uint32_t token = at - div_by(at, p.cache.page_tokens) * p.cache.page_tokens.d;
+                const uint64_t from =
+                    uint64_t(id) * p.cache.page_bytes + uint64_t(token + row0) * p.cache.row_bytes + head_off;
+                const uint32_t dst = ring + slot * C::STAGE + row0 * C::PITCH + piece * 16;
+                if (!has_piece) return;
+                const uint8_t *k = p.cache.k + from, *v = p.cache.v + from;
+#pragma unroll
+                for (uint32_t r = 0; r < kPlaces; r += ROWS) {
+                    cp_async16(dst + r * C::PITCH, k + r * p.cache.row_bytes, true);
+                    cp_async16(dst + (kPlaces + r) * C::PITCH, v + r * p.cache.row_bytes, true);
+                }
+            } else {
+                issue(slot, offset(step, id));
+            }
+        };
         int32_t id[kAhead];
         {
             int32_t first[C::STAGES - 1];
@@ -169,7 +186,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
 #pragma unroll
             for (int i = 0; i < C::STAGES - 1; ++i) {
                 const uint32_t step = warp + i * kSplitWarps;
-                if (step < steps) issue(i, offset(step, first[i]));
+                if (step < steps) issue_step(i, step, first[i]);
                 cp_commit();
             }
         }
@@ -238,7 +255,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
             {
                 const uint32_t ahead = step + (C::STAGES - 1) * kSplitWarps;
                 const uint32_t to = slot == 0 ? C::STAGES - 1 : slot - 1;
-                if (ahead < steps) issue(to, offset(ahead, id[0]));
+                if (ahead < steps) issue_step(to, ahead, id[0]);
                 cp_commit();
 #pragma unroll
                 for (int i = 1; i < kAhead; ++i) id[i - 1] = id[i];
@@ -535,7 +552,7 @@ template <int DT>
 sz_status run_dim(const AttnParams &p, int num_sms, cudaStream_t stream) {
     const uint32_t d = p.cache.head_dim;
     const uint64_t rows = cdiv(p.tokens, p.cache.seqs) * p.group.d;
-    if (d <= 128 && rows > 64) return launch_attn_tc(p, DT, num_sms, stream);
+    if (d <= 128 && rows > 32) return launch_attn_tc(p, DT, num_sms, stream);
     if (d <= 64) return rows <= 16 ? run<DT, 64, 1>(p, num_sms, stream) : run<DT, 64, 2>(p, num_sms, stream);
     if (d <= 128) return rows <= 16 ? run<DT, 128, 1>(p, num_sms, stream) : run<DT, 128, 2>(p, num_sms, stream);
     return run<DT, 256, 1>(p, num_sms, stream);
