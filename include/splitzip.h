@@ -95,7 +95,8 @@ typedef enum {
     SZ_ERR_BUFFER_TOO_SMALL = 3,  /* workspace or output capacity too small                       */
     SZ_ERR_CORRUPT_STREAM = 4,    /* stream fails a consistency check on decode                   */
     SZ_ERR_CUDA = 5,              /* a CUDA runtime call failed                                    */
-    SZ_ERR_TIMEOUT = 6,           /* the escape-offset look-back waited longer than its limit      */
+    SZ_ERR_TIMEOUT = 6,           /* the escape-offset look-back, or a wait of sz_attn_paged,        */
+                                  /* took longer than its limit                                    */
     SZ_ERR_PLAN_MISMATCH = 7,     /* encode data or sizes disagree with the plan                   */
     SZ_ERR_INTERNAL = 8           /* an internal consistency check failed                          */
 } sz_status;
@@ -336,8 +337,9 @@ sz_status sz_encode_noalloc(sz_dtype dtype, const sz_plan_t *d_plan, const void 
  * nearest, ties to even; beyond E5M2's range that is infinity, as in torch's
  * conversion).  The conventions at the top of this file hold here too; the
  * structs below are host data, read during the call.  d_ws is sized by
- * sz_ops_workspace_bytes and zeroed once by sz_workspace_init; it may be shared
- * with the codec's calls on the same stream if it is large enough for both. */
+ * sz_ops_workspace_bytes and zeroed once by sz_workspace_init.  It is the
+ * operators' own: not to be used by the codec's calls too, whose layout of a
+ * workspace is another. */
 
 /* A paged cache of `seqs` sequences.  Token t of sequence s has its key (all
  * heads) at
