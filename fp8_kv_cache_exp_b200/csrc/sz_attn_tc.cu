@@ -819,30 +819,29 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
                 const uint32_t at = (t.block0 + j) * kTcBlock;
                 const bool masked = at < full_lo || at + kTcBlock > full_hi;
                 uint32_t x[128];
-                if (masked) {
-                    // columns [a, b) of the block are seen; the others' scores become -infinity where they are
-                    const uint32_t a = rr.lo > at ? rr.lo - at : 0, b = rr.hi > at ? rr.hi - at : 0;
-                    for (uint32_t g = 0; g < 128; g += 16) {
-                        tc_ld16(x, s_at + g);
-                        tc_wait_ld();
-                        tc_arrived(x);
-                        const uint32_t ga = a > g ? min(a - g, 16u) : 0, gb = b > g ? min(b - g, 16u) : 0;
-                        const uint32_t seen = ((1u << gb) - 1) & (~0u << ga);
-#pragma unroll
-                        for (uint32_t c = 0; c < 16; ++c)
-                            if (!(seen & (1u << c))) x[c] = 0xff800000u;
-                        tc_st16(s_at + g, x);
-                    }
-                    tc_wait_st();
-                }
                 tc_ld32(x, s_at);
                 tc_ld32(x + 32, s_at + 32);
                 tc_wait_ld();
                 tc_ld32(x + 64, s_at + 64);
                 tc_ld32(x + 96, s_at + 96);
-                // (the first half's maximum while the second half comes)
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) tc_arrived(x + c);
+                if (masked) {
+                    // columns [a, b) of the block are seen; the others' scores become -infinity
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 64; c < 128; c += 16) tc_arrived(x + c);
+                    const uint32_t a = rr.lo > at ? rr.lo - at : 0, b = rr.hi > at ? rr.hi - at : 0;
+#pragma unroll
+                    for (uint32_t g = 0; g < 128; g += 32) {
+                        const uint32_t ga = a > g ? min(a - g, 32u) : 0, gb = b > g ? min(b - g, 32u) : 0;
+                        const uint32_t seen = uint32_t((1ull << gb) - 1) & uint32_t(~0ull << ga);
+#pragma unroll
+                        for (uint32_t c = 0; c < 32; ++c)
+                            if (!(seen & (1u << c))) x[g + c] = 0xff800000u;
+                    }
+                }
+                // (the first half's maximum while the second half comes)
                 float tops[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
