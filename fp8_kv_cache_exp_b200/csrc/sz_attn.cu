@@ -7,6 +7,12 @@
 // is rounded to the type that v is multiplied in (bf16, or fp16 for an E5M2
 // cache).
 //
+// Measured: 64 sequences of up to 8192 places, 32 heads on 8 of 128: 237 us, 5.6
+// TB/s, 0.86 of a plain copy's rate; one sequence of 131,072 places, 32 heads on
+// 4 in E5M2: 53 us, of which about 25 are fixed (the deal, the first pages' ids
+// and rows, the joining of 111 parts a head); one token over 777 places: 10 us,
+// all of it the latency of those steps.
+//
 // With few rows to a key the cache's bytes are the bound.  Each warp streams
 // its own places, 16 at a time, through its own ring of asynchronous copies
 // and waits for no other warp until its part of the tile is done; four warps
@@ -552,6 +558,9 @@ template <int DT>
 sz_status run_dim(const AttnParams &p, int num_sms, cudaStream_t stream) {
     const uint32_t d = p.cache.head_dim;
     const uint64_t rows = cdiv(p.tokens, p.cache.seqs) * p.group.d;
+    // Rows of a sequence and KV head, on average.  20 (8 sequences of 5 tokens, groups of 4,
+    // 8192 places): 58 us here, 74 in tensor memory; 64 (4 of 16 tokens, 4096 places): 68 and 44;
+    // one sequence of 16 tokens over 65,536: 232 and 82.  Wider heads' sums do not fit there twice.
     if (d <= 128 && rows > 32) return launch_attn_tc(p, DT, num_sms, stream);
     if (d <= 64) return rows <= 16 ? run<DT, 64, 1>(p, num_sms, stream) : run<DT, 64, 2>(p, num_sms, stream);
     if (d <= 128) return rows <= 16 ? run<DT, 128, 1>(p, num_sms, stream) : run<DT, 128, 2>(p, num_sms, stream);
