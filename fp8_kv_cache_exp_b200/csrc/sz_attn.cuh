@@ -90,7 +90,9 @@ struct Work {
     uint32_t more;          // ... and the number of CTAs, the first ones, that have one more
     uint32_t head, seq, tile;
     uint32_t from;          // the block of the tile at which `at` stands
+    uint32_t whole;         // not 0: whole tiles, so many to a head; then `at` counts this CTA's
 };
+constexpr uint32_t kFewTiles = 32;  // of a head, for work_begin_few
 
 template <int NT>
 struct WorkScratch {
@@ -134,11 +136,32 @@ __device__ __forceinline__ uint64_t work_share(const AttnParams &p, uint64_t per
     return w.at - w.head * per_head;
 }
 
+// Whole tiles of a head in `order` (sequence << 8 | tile), the longest first: CTA
+// c of C has every C-th of all heads' tiles, forwards and backwards in turn.
+__device__ __forceinline__ bool work_whole(const AttnParams &p, Work &w, const uint16_t *order) {
+    const uint64_t row = w.at * gridDim.x;
+    const uint64_t x = row + ((w.at & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (x >= uint64_t(w.whole) * p.cache.kv_heads) return false;
+    const uint32_t rank = uint32_t(x) / p.cache.kv_heads;
+    w.head = uint32_t(x) - rank * p.cache.kv_heads;
+    w.seq = order[rank] >> 8;
+    w.tile = order[rank] & 255;
+    w.from = 0;
+    return true;
+}
+
 // The same for at most 32 sequences with at most 32 tiles together, each warp by
 // itself: the block's way (below) costs a call of one token 2 us.  Says whether
 // it was possible; then `has` is whether the CTA has a share.
+//
+// With `order`, tiles of at most kWholeMost blocks that are at least as many as
+// the CTAs are not cut: a part of a tile costs its queries, its results and their
+// joining, as much as three to four blocks, and cutting saves half a tile (two
+// 1024-token prompts of 32 heads of 80: 40 us whole, 48 cut).  (All
+// threads call it then, and each has `order` behind the next barrier.)
+constexpr uint32_t kWholeMost = 8;
 template <int TR, int BN, int EXTRA>
-__device__ __forceinline__ bool work_begin_few(const AttnParams &p, Work &w, bool &has) {
+__device__ __forceinline__ bool work_begin_few(const AttnParams &p, Work &w, bool &has, uint16_t *order) {
     const uint32_t lane = threadIdx.x & 31, seqs = p.cache.seqs;
     if (seqs > 32) return false;
     SeqInfo si{0, 0, 0};
@@ -166,6 +189,22 @@ __device__ __forceinline__ bool work_begin_few(const AttnParams &p, Work &w, boo
     const uint32_t tile = lane - __shfl_sync(0xffffffffu, ends - tiles, int(seq));
     const uint32_t units =
         lane < count ? EXTRA + range_blocks<BN>(tile_range<TR>(p, SeqInfo{0, q_len, kv}, tile)) : 0;
+    w.whole = 0;
+    if (order && uint64_t(count) * p.cache.kv_heads >= gridDim.x &&
+        !__any_sync(0xffffffffu, units > EXTRA + kWholeMost)) {
+        uint32_t rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t other = __shfl_sync(0xffffffffu, units, j);
+            rank += other > units || (other == units && j < int(lane));
+        }
+        if (threadIdx.x < 32 && lane < count) order[rank] = uint16_t(seq << 8 | tile);
+        w.whole = count;
+        w.at = 0;
+        __syncthreads();
+        has = work_whole(p, w, order);
+        return true;
+    }
     uint64_t to = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -185,9 +224,10 @@ __device__ __forceinline__ bool work_begin_few(const AttnParams &p, Work &w, boo
 
 // The CTA's share; false if it has none.  All NT threads call it.
 template <int NT, int TR, int BN, int EXTRA>
-__device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w) {
+__device__ bool work_begin(const AttnParams &p, WorkScratch<NT> &s, Work &w, uint16_t *order = nullptr) {
     bool has;
-    if (work_begin_few<TR, BN, EXTRA>(p, w, has)) return has;
+    if (work_begin_few<TR, BN, EXTRA>(p, w, has, order)) return has;
+    w.whole = 0;
     const uint32_t tid = threadIdx.x, seqs = p.cache.seqs;
     // this thread's tile of the chunk looked at last
     uint32_t seq = 0, tile = 0, units = 0, chunks = 0;
@@ -279,7 +319,7 @@ __device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w, ui
     t.rows = min(uint32_t(TR), t.s.q_len * p.group.d - t.r0);
     t.block0 = t.r.lo / BN;
     t.n = range_blocks<BN>(t.r);
-    const uint32_t to = uint32_t(min(uint64_t(EXTRA + t.n), w.from + (w.end - w.at)));
+    const uint32_t to = w.whole ? EXTRA + t.n : uint32_t(min(uint64_t(EXTRA + t.n), w.from + (w.end - w.at)));
     t.count = to - w.from;
     t.from = w.from > EXTRA ? w.from - EXTRA : 0;
     t.to = to - EXTRA;  // (work_begin and work_next leave no part without blocks of its own)
@@ -295,7 +335,11 @@ __device__ __forceinline__ Part work_part(const AttnParams &p, const Work &w, ui
 
 // On to the next tile; false at the end of the share.
 template <int TR, int EXTRA>
-__device__ __forceinline__ bool work_next(const AttnParams &p, Work &w, const Part &t) {
+__device__ __forceinline__ bool work_next(const AttnParams &p, Work &w, const Part &t, const uint16_t *order = nullptr) {
+    if (w.whole) {
+        ++w.at;
+        return work_whole(p, w, order);
+    }
     w.at += t.count;
     if (w.at + EXTRA >= w.end) return false;
     w.from = 0;

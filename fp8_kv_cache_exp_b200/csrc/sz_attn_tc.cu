@@ -20,7 +20,7 @@
 // blocks leave them where they are.
 //
 // Measured: 2048 tokens over 8192 places, 32 heads on 8 of 128: 257 us, 0.94
-// PFLOP/s; two 1024-token prompts of 32 heads of 80: 48 us; five ragged chunks of
+// PFLOP/s; two 1024-token prompts of 32 heads of 80: 40 us; five ragged chunks of
 // up to 700 tokens, window 1024, 32 heads on 4 in E5M2: 82 us.
 //
 // What bounds it: a block of 256 rows and heads of 128 is 2048 clocks of matrix
@@ -99,6 +99,7 @@ struct TcAux {
     uint64_t turn[2];                  // a tile's turn at ex2
     uint64_t drain[2];
     uint32_t tmem, abort, bad;
+    uint16_t order[kFewTiles];
 };
 static_assert(sizeof(TcAux) <= 1024, "aux");
 
@@ -109,6 +110,7 @@ struct TcDesc {
     uint32_t bad;    // rows of its own tiles came out not finite
     uint32_t joins;  // `join` is one
     uint32_t has, pad;
+    uint16_t order[kFewTiles];
 };
 static_assert(sizeof(TcDesc) * kMaxSms <= kDescBytes, "descriptors");
 
@@ -462,7 +464,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
                 }
                 raws += tiles;
             }
-            if (!work_next<kTcRows, kTcExtra>(p, w, t)) return;
+            if (!work_next<kTcRows, kTcExtra>(p, w, t, aux->order)) return;
             continue;
         }
         int32_t id = page_id(t.from);
@@ -518,7 +520,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
             }
             cp_wait<0>();
         }
-        if (!work_next<kTcRows, kTcExtra>(p, w, t)) return;
+        if (!work_next<kTcRows, kTcExtra>(p, w, t, aux->order)) return;
     }
 }
 
@@ -591,7 +593,7 @@ __device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMa
             bar_arrive(bar);
             __syncwarp();
         }
-        if (!work_next<kTcRows, kTcExtra>(p, w, t)) return;
+        if (!work_next<kTcRows, kTcExtra>(p, w, t, aux->order)) return;
     }
 }
 
@@ -638,7 +640,7 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
         Part after = t;  // the next part, found while the first scores are on their way
         bool more = false;
         auto look_ahead = [&]() {
-            more = work_next<kTcRows, kTcExtra>(p, w, t);
+            more = work_next<kTcRows, kTcExtra>(p, w, t, aux->order);
             if (more) after = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
         };
         if (i * 128 < t.rows) {
@@ -774,7 +776,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
         Part after = t;
         bool more = false;
         auto look_ahead = [&]() {
-            more = work_next<kTcRows, kTcExtra>(p, next, t);
+            more = work_next<kTcRows, kTcExtra>(p, next, t, aux->order);
             if (more) after = work_part<kTcRows, kTcBlock, kTcExtra>(p, next, blockIdx.x);
         };
         const uint32_t parts = t.c_last - t.c_first + 1;
@@ -1029,13 +1031,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_launch_dependents();
     Work w;
     const bool has = work_begin<kTcThreads, kTcRows, kTcBlock, kTcExtra>(
-        p, *reinterpret_cast<WorkScratch<kTcThreads> *>(smem + C::RING_AT), w);
+        p, *reinterpret_cast<WorkScratch<kTcThreads> *>(smem + C::RING_AT), w, aux->order);
     if (tid == 0) {
         desc->joins = 0;
         desc->has = has;
         desc->bad = 0;
         if (has) desc->begin = w;
     }
+    if (has && tid < kFewTiles) desc->order[tid] = w.whole ? aux->order[tid] : 0;
     if (!has) return;
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&aux->tmem))
@@ -1210,7 +1213,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
                     for (uint32_t e = lane; e < d; e += 32) bad = bad || (out[e] & 0x7f80u) == 0x7f80u;
                     if (__any_sync(0xffffffffu, bad)) repair_row<DT>(p, t.s, w.seq, w.head, g, t.r);
                 }
-            if (!work_next<kTcRows, kTcExtra>(p, w, t)) break;
+            if (!work_next<kTcRows, kTcExtra>(p, w, t, descs[c].order)) break;
         }
     }
 }

@@ -143,7 +143,7 @@ constexpr uint32_t kAttnCtas = 3 * kMaxSms;  // most CTAs of any attention kerne
 // counters: three for each CTA of the split kernel, or one for each warp of a tile
 constexpr size_t kArrivedBytes = size_t(3) * kAttnCtas * 4;
 static_assert(kMaxSms * 8 <= 3 * kAttnCtas, "arrival counters");
-constexpr size_t kDescBytes = size_t(kMaxSms) * 128;
+constexpr size_t kDescBytes = size_t(kMaxSms) * 192;
 // floats of all partials: the largest (CTAs * rows) of the kernels is a
 // persistent CTA for each SM with 256 rows, or kAttnCtas of 32
 constexpr size_t attn_part_floats(uint32_t head_dim) { return size_t(2) * kMaxSms * 256 * (head_dim + 2); }

@@ -208,3 +208,26 @@ def test_the_binding_refuses_what_does_not_fit():
     with pytest.raises(m.SplitZipError):
         m.sz_qk_norm_rope(q, None, torch.empty_like(q), None, ws, rope=torch.zeros(10, 64, device="cuda"))
     assert m.sz_last_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim,window", [
+    ([140, 200, 33], [140, 300, 900], 64, 64, 64, 0), ([300], [300], 160, 160, 16, 0), ([1024, 700], [1024, 700], 32, 32, 80, 0),
+    ([70, 0, 1, 500], [1000, 3, 1, 1024], 160, 40, 32, 0), ([600], [600], 64, 64, 48, 100), ([100] * 32, [100 + i for i in range(32)], 8, 8, 64, 0)])
+def test_tiles_that_are_not_cut(dtype, q_lens, kv_lens, heads, kv_heads, dim, window):
+    """Short tiles, at least as many as the SMs: each by one CTA, the longest first."""
+    check_attention(sz(), dtype, q_lens, kv_lens, heads, kv_heads, dim, 16, window=window, seed=dim, tail=1)
+
+
+def test_values_that_are_not_finite_in_tiles_that_are_not_cut():
+    m, g = sz(), gen(29)
+    n, heads = 300, 160
+    c = P.build_cache(g, BF16, [n], 16, heads, 16)
+    at = 150
+    c.v_pool[int(c.table[0, at // 16]), at % 16] = math.nan
+    q = torch.randn(n, heads, 16, generator=g).bfloat16()
+    out, lse = run_attention(m, c, q.cuda(), [n], [n])
+    ref, rl, mag, reach = P.attention(q[:at], c.k[0][:at], c.v[0][:at])
+    close(out[:at], ref, P.attention_bound(ref, mag, reach, False), "rows that do not see it")
+    close(lse[:at], rl, 2.0 ** -18 * (reach + rl.abs()) + 2.0 ** -16, "their lse")
+    assert torch.isnan(out[at:]).all()
