@@ -8,17 +8,17 @@
 //
 // One element is read, turned and written: the bytes are the bound, and for a
 // few tokens the latency of the dependent loads (sequence, length, page id).
-// Measured: 16,384 tokens of 40 heads of 128, normed: 71 us, 4.9 TB/s, 0.74 of a
+// Measured: 16,384 tokens of 40 heads of 128, normed: 67 us, 5.1 TB/s, 0.78 of a
 // plain copy's rate (positions and their table rows are two loads in a row, and
-// 24 warps an SM do not hide all of it: 64 registers a thread or 2 rows to a
-// group change nothing); chunks of 6 prompts into an E5M2 cache: 22 us; one
+// 24 warps an SM do not hide all of it; 64 registers a thread or other numbers of
+// rows to a group are slower); chunks of 6 prompts into an E5M2 cache: 21 us; one
 // token: 2.7 us, the call itself.
 #include "sz_ops.cuh"
 
 namespace sz {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;  // six CTAs an SM turn over more evenly than three of 256 (16,384 tokens: 67 us, 71)
 
 // Plain loads: the rows may be those that the call writes (in place, each lane
 // writes the elements that it read).
@@ -93,7 +93,7 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
 // on their way before anything that they wait for.  Runs of 8 bytes (below) took
 // 109 us for 16,384 tokens of 40 heads of 128.
 template <int LG, int N, bool APPEND, int DT>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_wide_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_wide_kernel(const __grid_constant__ RopeParams p) {
     constexpr uint32_t EB = DT == SZ_BF16 ? 2 : 1;
     pdl_wait();
     pdl_launch_dependents();
