@@ -4,7 +4,9 @@
 //
 //   n_i = x_i * (1 / sqrt(mean(x^2) + eps)) * w_i
 //   (a, b) -> (a cos - b sin, b cos + a sin) for the pairs of the first rot
-//   elements, in 32 bits, rounded once to the output's type.
+//   elements, in 32 bits, rounded once to the output's type.  Each product and
+//   sum of the rotation is rounded by itself: fused, some keys next to the border
+//   of two 8-bit values would fall on its other side than the formula in 32 bits.
 //
 // One element is read, turned and written: the bytes are the bound, and for a
 // few tokens the latency of the dependent loads (sequence, length, page id).
@@ -76,8 +78,8 @@ __device__ __forceinline__ bool locate(const RopeParams &p, uint32_t token, bool
 
 __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
     const float u = a, v = b;
-    a = fmaf(u, c, -(v * s));
-    b = fmaf(v, c, u * s);
+    a = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
+    b = __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s));
 }
 __device__ __forceinline__ void unpack8(float *x, const uint4 &v) {
     x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
