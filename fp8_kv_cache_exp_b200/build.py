@@ -71,8 +71,8 @@ def build_host(force: bool = False, verbose: bool = False) -> str:
     return HOST
 
 
-def build(force: bool = False, extra_flags=(), out: str = LIB, verbose: bool = False) -> str:
-    """Compile every csrc/*.cu (one nvcc per file, in parallel) and link them
+def build(force: bool = False, extra_flags=(), out: str = LIB, verbose: bool = False, files=None) -> str:
+    """Compile every csrc/*.cu, or the named ones (one nvcc per file, in parallel), and link them
     into one shared library; return its path."""
     if out == LIB:
         build_host(force, verbose)
@@ -90,7 +90,7 @@ def build(force: bool = False, extra_flags=(), out: str = LIB, verbose: bool = F
                 print(" ".join(cmd))
             subprocess.run(cmd, check=True)
             return obj
-        srcs = sources()
+        srcs = sources() if files is None else [os.path.join(CSRC, f) for f in files]
         with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
             objs = list(ex.map(compile_one, srcs))
         cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]

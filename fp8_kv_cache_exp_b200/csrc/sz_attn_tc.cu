@@ -54,7 +54,18 @@
 namespace sz {
 namespace {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+// A wait's limit, 2 s, and how many polls lie between two looks at the clock and at
+// whether another role has given up.  A copy of the library that tests giving up
+// sets both otherwise (one poll: of the kind that does not suspend the thread).
+#ifndef SZ_ATTN_WAIT_NS
+#define SZ_ATTN_WAIT_NS 2000000000ull
+#endif
+#ifndef SZ_ATTN_POLLS
+#define SZ_ATTN_POLLS 64
+#endif
+// What is under way when a CTA leaves is waited for, whether or not it has given up:
+// microseconds, unless another warp's arrival at the same barrier never comes.
+constexpr uint64_t kLandLimitNs = 5000000ull;  // 5 ms
 
 constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;
@@ -114,16 +125,25 @@ struct TcDesc {
 };
 static_assert(sizeof(TcDesc) * kMaxSms <= kDescBytes, "descriptors");
 
+__device__ __forceinline__ bool bar_poll(uint64_t *bar, uint32_t parity) {
+    if constexpr (SZ_ATTN_POLLS > 1) return mbar_try_wait(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Waits are bounded: after the limit the CTA gives up (every role then leaves
 // its loop) and the error word says so.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, TcAux *aux, uint32_t *ctl) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, TcAux *aux, uint32_t *ctl, uint64_t limit) {
+    if (bar_poll(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63) == 0) {
+        if (bar_poll(bar, parity)) return true;
+        if (i % SZ_ATTN_POLLS == 0) {
             if (*reinterpret_cast<volatile uint32_t *>(&aux->abort)) return false;
-            if (global_ns() - t0 > kWaitLimitNs) {
+            if (global_ns() - t0 > limit) {
                 *reinterpret_cast<volatile uint32_t *>(&aux->abort) = 1;
                 set_error(ctl, SZ_ERR_TIMEOUT, blockIdx.x);
                 return false;
@@ -132,8 +152,8 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, TcAux *
     }
 }
 // All lanes wait, and go on together.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, TcAux *aux, uint32_t *ctl) {
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, aux, ctl));
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, TcAux *aux, const AttnParams &p) {
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, aux, p.ctl, p.wait_ns));
 }
 __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -298,8 +318,10 @@ __device__ __forceinline__ void spread16(uint32_t block, uint32_t row, uint32_t 
     sts_u128(a + (((ch + (odd ? 0 : 1)) ^ (row & 7)) << 4), odd ? lo : hi);
 }
 
+// `issued`: stages filled; `raws`: tiles fetched into the raw ring.
 template <int DT, int DP>
-__device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps, Work w, uint32_t base, TcAux *aux) {
+__device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps, Work w, uint32_t base, TcAux *aux,
+                                           uint32_t &issued, uint32_t &raws) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t LPR = DP * C::EB / 16;  // lanes to a row of the cache
     constexpr uint32_t ROWS = 32 / LPR;        // rows to an instruction
@@ -308,8 +330,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
     const uint32_t d = p.cache.head_dim;
     const uint32_t piece = lane % LPR, row0 = warp * 32 + lane / LPR;
     const bool has_piece = piece * 16 < d * C::EB;
-    uint32_t raws = 0;               // tiles that have gone through the raw ring
-    uint32_t issued = 0, ready = 0;  // what is behind `ready` has been handed over
+    uint32_t ready = 0;  // what is behind `ready` has been handed over
     auto hand_over = [&](uint32_t to) {
         if (ready == to) return;
         fence_proxy_async_smem();
@@ -321,12 +342,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
         return bool(__all_sync(0xffffffffu, mbar_try_wait(&aux->empty[n % C::STAGES], (n / C::STAGES - 1) & 1)));
     };
     auto wait_free = [&](uint32_t n) {
-        return n < C::STAGES || warp_wait(&aux->empty[n % C::STAGES], (n / C::STAGES - 1) & 1, aux, p.ctl);
-    };
-    // before giving up: the tensor copies that are under way land, or a limit passes
-    auto land = [&](uint64_t *bars, uint32_t ring, uint32_t n) {
-        for (uint32_t x = n > ring ? n - ring : 0; x < n; ++x)
-            for (uint32_t i = 0; i < 1u << 16 && !mbar_try_wait(&bars[x % ring], (x / ring) & 1); ++i) {}
+        return n < C::STAGES || warp_wait(&aux->empty[n % C::STAGES], (n / C::STAGES - 1) & 1, aux, p);
     };
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
@@ -422,30 +438,23 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
             };
             if constexpr (DT == SZ_BF16) {
                 for (uint32_t n = 0; n < tiles; ++n, ++issued) {
-                    if (!wait_free(issued)) {
-                        land(aux->full, C::STAGES, issued);
-                        return;
-                    }
+                    if (!wait_free(issued)) return;
                     next_fetch(n, base + C::RING_AT + (issued % C::STAGES) * C::STAGE, C::STAGE,
                                &aux->full[issued % C::STAGES]);
                 }
                 ready = issued;
             } else {
+                const uint32_t raw0 = raws;
                 for (uint32_t n = 0; n < tiles + C::RAWS - 1; ++n) {
                     if (n < tiles) {
-                        const uint32_t x = raws + n, slot = x % C::RAWS;
-                        if (x >= C::RAWS && !warp_wait(&aux->raw_empty[slot], (x / C::RAWS - 1) & 1, aux, p.ctl)) {
-                            land(aux->raw_full, C::RAWS, raws + n);
-                            return;
-                        }
+                        const uint32_t slot = raws % C::RAWS;
+                        if (raws >= C::RAWS && !warp_wait(&aux->raw_empty[slot], (raws / C::RAWS - 1) & 1, aux, p)) return;
                         next_fetch(n, base + C::RAW_AT + slot * C::RAW, C::RAW, &aux->raw_full[slot]);
+                        ++raws;
                     }
                     if (n + 1 < C::RAWS || n + 1 - C::RAWS >= tiles) continue;
-                    const uint32_t x = raws + n + 1 - C::RAWS, slot = x % C::RAWS;
-                    if (!warp_wait(&aux->raw_full[slot], (x / C::RAWS) & 1, aux, p.ctl) || !wait_free(issued)) {
-                        land(aux->raw_full, C::RAWS, raws + min(n + 1, tiles));
-                        return;
-                    }
+                    const uint32_t x = raw0 + n + 1 - C::RAWS, slot = x % C::RAWS;
+                    if (!warp_wait(&aux->raw_full[slot], (x / C::RAWS) & 1, aux, p) || !wait_free(issued)) return;
                     if (has_piece) {
 #pragma unroll
                         for (uint32_t u0 = 0; u0 < N; u0 += 4) {
@@ -462,7 +471,6 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
                     ++issued;
                     hand_over(issued);
                 }
-                raws += tiles;
             }
             if (!work_next<kTcRows, kTcExtra>(p, w, t, aux->order)) return;
             continue;
@@ -524,30 +532,37 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
     }
 }
 
+template <int DT, int DP>
+__device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps, const Work &w, uint32_t base, TcAux *aux) {
+    using C = TcCfg<DT, DP>;
+    uint32_t issued = 0, raws = 0;
+    load_parts<DT, DP>(p, maps, w, base, aux, issued, raws);
+    cp_wait<0>();
+    // the tensor copies that are under way land (nobody else waits for them where the CTA gives up)
+    if (maps.box == 0 || (threadIdx.x & 127) >= 32) return;
+    uint64_t *bars = DT == SZ_BF16 ? aux->full : aux->raw_full;
+    const uint32_t ring = DT == SZ_BF16 ? C::STAGES : C::RAWS, n = DT == SZ_BF16 ? issued : raws;
+    for (uint32_t x = n > ring ? n - ring : 0; x < n; ++x) mbar_wait(&bars[x % ring], (x / ring) & 1, kLandLimitNs);
+}
+
 // Queries into shared memory (warps 14, 15): by tensor copies of 128 / G tokens
 // of the group's G heads where G divides 128 (`map`; rows behind the sequence's
 // last are then the next one's, and nobody's), or row by row.
 constexpr uint32_t kQueryWarps = 2;
 template <int DT, int DP>
-__device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMap *map, Work w, uint32_t base, TcAux *aux) {
+__device__ __forceinline__ void query_parts(const AttnParams &p, const CUtensorMap *map, Work w, uint32_t base, TcAux *aux,
+                                            uint32_t &seen, uint32_t &phases) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t QL = DP / 8, QR = 32 / QL;          // lanes to a row, rows to an instruction
     constexpr uint32_t BATCH = 8;
     const uint32_t lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 14, c = lane % QL;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
-    uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i]
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
         const uint8_t *q = p.q.p + uint64_t(t.s.q0) * p.q.ts + uint64_t(w.head * G) * p.q.hs;
         for (uint32_t i = 0; i * 128 < t.rows; ++i) {
             if (seen & (1u << i)) {
-                if (!warp_wait(&aux->q_empty[i], (phases >> i) & 1, aux, p.ctl)) {
-                    // giving up: tensor copies that are under way land, or a limit passes
-                    uint64_t *here = DT == SZ_BF16 ? aux->q_full : aux->q_here;
-                    for (uint32_t x = 0; map && x < 2; ++x)
-                        for (uint32_t n = 0; (seen >> x & 1) && n < 1u << 16 && !mbar_try_wait(&here[x], (phases >> x) & 1); ++n) {}
-                    return;
-                }
+                if (!warp_wait(&aux->q_empty[i], (phases >> i) & 1, aux, p)) return;
                 phases ^= 1u << i;
             }
             seen |= 1u << i;
@@ -597,27 +612,38 @@ __device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMa
     }
 }
 
+template <int DT, int DP>
+__device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMap *map, const Work &w, uint32_t base,
+                                           TcAux *aux) {
+    uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i], and of the last copy
+    query_parts<DT, DP>(p, map, w, base, aux, seen, phases);
+    cp_wait<0>();
+    if (!map || threadIdx.x / 32 != 14) return;
+    uint64_t *here = DT == SZ_BF16 ? aux->q_full : aux->q_here;
+    for (uint32_t i = 0; i < 2; ++i)
+        if (seen >> i & 1) mbar_wait(&here[i], (phases >> i) & 1, kLandLimitNs);
+}
+
 // The products of tile i (warps 12 and 13).  A warp goes through the loop
 // together and one elected lane issues: behind a test of the thread's own number
 // the compiler does not see that one lane is left, and each product took twice
 // as long.  All of tensor memory is this CTA's, so its addresses are constants.
 template <int DT, int DP>
-__device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux, uint32_t i) {
+__device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t base, TcAux *aux, uint32_t i, bool leader) {
     using C = TcCfg<DT, DP>;
     const uint32_t d = p.cache.head_dim, ksteps = d / 16;
     const uint32_t qk_desc = instr_desc(DT, kTcBlock, false), pv_desc = instr_desc(DT, d, true);
-    const bool leader = elect_one();
     uint32_t kv = 0;      // the part's first stage
     uint32_t phases = 0;  // bit 2: of q_full[i]; bit h: of p_full[i][h]
     const uint64_t qd = smem_desc(base + i * C::QTILE);
     auto wait = [&](uint64_t *bar, uint32_t bit) {
-        const bool ok = warp_wait(bar, (phases >> bit) & 1, aux, p.ctl);
+        const bool ok = warp_wait(bar, (phases >> bit) & 1, aux, p);
         phases ^= 1u << bit;
         tc_after();
         return ok;
     };
     auto full = [&](uint32_t n) {
-        const bool ok = warp_wait(&aux->full[n % C::STAGES], (n / C::STAGES) & 1, aux, p.ctl);
+        const bool ok = warp_wait(&aux->full[n % C::STAGES], (n / C::STAGES) & 1, aux, p);
         tc_after();
         return ok;
     };
@@ -794,7 +820,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
             float sc = p.scale_log2;
             if constexpr (DT == SZ_FP8_E5M2) {
                 // the row's queries to fp16, behind a power of two that its scores are divided by
-                if (!warp_wait(&aux->q_here[i], q_uses++ & 1, aux, p.ctl)) return;
+                if (!warp_wait(&aux->q_here[i], q_uses++ & 1, aux, p)) return;
                 const uint32_t at = base + i * C::QTILE + row * 128;
                 const auto chunk = [&](uint32_t c) { return at + (c / 8) * kQPanel + (((c % 8) ^ (row & 7)) << 4); };
                 uint32_t big = 0;  // of magnitudes as 16-bit integers, whose order is that of the numbers
@@ -823,7 +849,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
             }
             float m = -INFINITY, l = 0.f;
             for (uint32_t j = t.from; j < t.to; ++j) {
-                if (!warp_wait(&aux->s_full[i], s_uses++ & 1, aux, p.ctl)) return;
+                if (!warp_wait(&aux->s_full[i], s_uses++ & 1, aux, p)) return;
                 tc_after();
                 const uint32_t at = (t.block0 + j) * kTcBlock;
                 const bool masked = at < full_lo || at + kTcBlock > full_hi;
@@ -894,7 +920,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
                 // part of the ex2 made it 255: its multiply-adds, two to an instruction
                 // or not, take the issue slots.
                 if (t.rows > 128) {
-                    if ((i == 1 || turns > 0) && !warp_wait(&aux->turn[i], (turns - 1 + i) & 1, aux, p.ctl)) return;
+                    if ((i == 1 || turns > 0) && !warp_wait(&aux->turn[i], (turns - 1 + i) & 1, aux, p)) return;
                     ++turns;
                 }
                 const float shift = C::RAISE - (m == -INFINITY ? 0.f : m);
@@ -933,7 +959,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
                 l += a + b;
             }
             look_ahead();
-            if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p.ctl)) return;
+            if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p)) return;
             tc_after();
             if (whole_tile) {
                 const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
@@ -1055,21 +1081,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 " SZ_TC_REGS_SOFTMAX ";");
         softmax_role<DT, DP>(p, w, base, aux, desc);
+        __syncwarp();
+        tc_wait_st();  // (where the CTA gives up, sums may be on their way back)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " SZ_TC_REGS_OTHER ";");
         if (warp < 12) {
             load_role<DT, DP>(p, Maps{&k_map, &v_map, box}, w, base, aux);
-            cp_wait<0>();
         } else if (warp < 14) {
-            mma_role<DT, DP>(p, w, base, aux, warp - 12);
-            // nothing of this CTA's is under way when it gives its memory back
+            const bool leader = elect_one();
+            mma_role<DT, DP>(p, w, base, aux, warp - 12, leader);
+            // no product of this CTA's is under way when it gives its memory back, given up or not
             __syncwarp();
-            if (elect_one()) tc_commit(&aux->drain[warp - 12]);
+            if (leader) tc_commit(&aux->drain[warp - 12]);
             __syncwarp();
-            warp_wait(&aux->drain[warp - 12], 0, aux, p.ctl);
+            mbar_wait(&aux->drain[warp - 12], 0, kLandLimitNs);
+            __syncwarp();
         } else {
             query_role<DT, DP>(p, q_box ? &q_map : nullptr, w, base, aux);
-            cp_wait<0>();
         }
     }
     __syncwarp();
@@ -1288,7 +1316,8 @@ sz_status run(const AttnParams &p, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-sz_status launch_attn_tc(const AttnParams &p, int dtype, int num_sms, cudaStream_t stream) {
+sz_status launch_attn_tc(AttnParams p, int dtype, int num_sms, cudaStream_t stream) {
+    p.wait_ns = SZ_ATTN_WAIT_NS;
     if (dtype == SZ_BF16)
         return p.cache.head_dim <= 64 ? run<SZ_BF16, 64>(p, num_sms, stream) : run<SZ_BF16, 128>(p, num_sms, stream);
     return p.cache.head_dim <= 64 ? run<SZ_FP8_E5M2, 64>(p, num_sms, stream)

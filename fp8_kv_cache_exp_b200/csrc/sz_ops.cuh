@@ -72,6 +72,7 @@ struct AttnParams {
     float scale_log2;    // scale * log2(e)
     uint32_t tokens, causal, window;
     FastDiv group;       // query heads to a KV head
+    uint64_t wait_ns;    // limit of the tensor-memory kernel's waits
 };
 
 // ------------------------------------------------------------ device helpers
@@ -133,7 +134,7 @@ __device__ __forceinline__ uint32_t pack_e5m2(float lo, float hi) {
 // Launchers (sz_rope.cu, sz_attn.cu, sz_attn_tc.cu).
 sz_status launch_rope(const RopeParams &p, bool append, int dtype, int num_sms, cudaStream_t stream);
 sz_status launch_attn(const AttnParams &p, int dtype, int num_sms, cudaStream_t stream);
-sz_status launch_attn_tc(const AttnParams &p, int dtype, int num_sms, cudaStream_t stream);
+sz_status launch_attn_tc(AttnParams p, int dtype, int num_sms, cudaStream_t stream);
 
 // Workspace of sz_attn_paged behind the 256-byte control block: arrival
 // counters, descriptors, then partial results.  A partial is kPartRows rows of a head's
