@@ -45,7 +45,7 @@ struct SplitCfg {
     static constexpr int TR = 16 * MT;
     static constexpr int PITCH = DP * EB + 16;             // odd in 16-byte units: rows fall on different banks
     static constexpr int STAGE = 2 * kPlaces * PITCH;      // keys, then values
-        static constexpr int STAGES = DP > 128 ? 2 : (DP > 64 ? 3 : 5);
+    static constexpr int STAGES = DP > 128 ? 2 : (DP > 64 ? 3 : 5);
     static constexpr int RING = kSplitWarps * STAGES * STAGE;
     static constexpr int QPITCH = DP * 2 + 16;
     static constexpr int OPITCH = DP + 4;                  // floats
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ WorkScratch<kSplitThreads> s_work;
     __shared__ float s_m[kSplitWarps][TR], s_l[kSplitWarps][TR], s_rs[TR], s_M[TR], s_L[TR];
-    __shared__ uint32_t s_bad[TR], s_last;
+    __shared__ uint32_t s_edge, s_last;
 
     pdl_wait();
     pdl_launch_dependents();
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
     const uint32_t piece = lane % LPR, row0 = lane / LPR;
     const bool has_piece = piece * 16 < d * C::EB;
     const bool one_page = p.cache.page_tokens.d % kPlaces == 0;  // a step lies in one page
+    if (tid == 0) s_edge = 0;  // whether an edge held a value that is not finite
 
     Work w;
     if (!work_begin<kSplitThreads, TR, kSplitBlock, kSplitExtra>(p, s_work, w)) return;
@@ -224,19 +225,12 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
             }
             *reinterpret_cast<uint4 *>(s_q + r * C::QPITCH + c * 16) = v;
         }
-        if (tid < TR) s_bad[tid] = 0;
         __syncthreads();
 
         // this lane's rows: lane / 4 and + 8 of each 16
         uint32_t lo[MT][2], hi[MT][2];
         float sc[MT][2], m[MT][2], l[MT][2], o[MT][DP / 8][4];
-        uint32_t full_lo, full_hi;
-        {
-            const Range a = token_range(p, t.s, div_by(t.r0, p.group));
-            const Range b = token_range(p, t.s, div_by(t.r0 + t.rows - 1, p.group));
-            full_lo = b.lo;  // every row sees [full_lo, full_hi)
-            full_hi = a.hi;
-        }
+        const Range all = seen_by_all(p, t);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -313,7 +307,20 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
                 }
             }
             const uint32_t at = part_lo + step * kPlaces;
-            const bool whole = at >= full_lo && at + kPlaces <= full_hi;
+            const bool whole = at >= all.lo && at + kPlaces <= all.hi;
+            if (has_edges(all, max(at, t.r.lo), min(at + kPlaces, part_hi))) {
+#pragma unroll 1
+                for (uint32_t r = row0; r < kPlaces; r += ROWS) {
+                    const uint32_t c = at + r, a = vb + r * C::PITCH + piece * 16;
+                    if (!has_piece || (c >= all.lo && c < all.hi)) continue;
+                    uint4 v = lds_u128(a);
+                    if (make_finite<DT>(v)) {
+                        sts_u128(a, v);
+                        s_edge = 1;
+                    }
+                }
+                __syncwarp();
+            }
             uint32_t pa[MT][4];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -442,8 +449,6 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
             const uint32_t i = div_by(t.r0 + r, p.group), head = w.head * G + (t.r0 + r - i * G);
             const float f = L == 0.f ? 0.f : 1.f / L;
             v.x *= f, v.y *= f, v.z *= f, v.w *= f;
-            if (!(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY))
-                s_bad[r] = 1;
             *reinterpret_cast<uint2 *>(p.out.p + uint64_t(t.s.q0 + i) * p.out.ts + uint64_t(head) * p.out.hs + c * 8) =
                 make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
             if (c == 0 && p.lse)
@@ -458,6 +463,12 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
                 const float4 a = *reinterpret_cast<const float4 *>(s_o + (k * TR + r) * C::OPITCH + c * 4);
                 v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
             }
+            if (s_edge) {
+                float sum[4] = {v.x, v.y, v.z, v.w};
+                add_not_finite<DT, 4>(p, w.seq, w.head, token_range(p, t.s, div_by(t.r0 + r, p.group)), all, part_lo,
+                                      part_hi, c * 4, sum);
+                v = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            }
             if (whole_tile) {
                 finish(r, c, v, s_M[r], s_L[r]);
             } else {
@@ -468,7 +479,6 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
                 }
             }
         }
-        bool written = whole_tile;
         if (!whole_tile) {
             // Parts are joined by whoever comes last to them: of up to 16 at once, of more in
             // groups, and then the groups; one CTA that reads 111 parts takes 30 us.
@@ -526,19 +536,10 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const __grid_
             uint32_t *counter = mine == 0 ? p.arrived + t.c_first : p.arrived + kAttnCtas + t.c_first + mine * group;
             if (last_of(counter, min(group, parts - mine * group))) {
                 join(mine * group, 1, min(group, parts - mine * group), groups == 1);
-                written = groups == 1;
-                if (groups > 1 && last_of(p.arrived + 2 * kAttnCtas + t.c_first, groups)) {
-                    join(0, group, groups, true);
-                    written = true;
-                }
+                if (groups > 1 && last_of(p.arrived + 2 * kAttnCtas + t.c_first, groups)) join(0, group, groups, true);
             }
         }
         __syncthreads();
-        if (written && t.s.q_len > 1) {
-            for (uint32_t r = warp; r < t.rows; r += kSplitWarps)
-                if (s_bad[r]) repair_row<DT>(p, t.s, w.seq, w.head, t.r0 + r, t.r);
-            __syncthreads();
-        }
         if (!work_next<TR, kSplitExtra>(p, w, t)) break;
     }
 }

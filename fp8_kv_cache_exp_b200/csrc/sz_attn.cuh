@@ -1,5 +1,5 @@
 // sz_attn.cuh -- what the attention kernels share: how the work is cut and
-// shared out, how partial results are joined, and the exact path of a row.
+// shared out, how partial results are joined, and values that are not finite.
 //
 // A tile is TR rows of one sequence and one KV head: a row is a (token, query
 // head of the group) pair, row r being token r / G, head r % G, so that one
@@ -358,85 +358,93 @@ __device__ __forceinline__ bool work_next(const AttnParams &p, Work &w, const Pa
 // CTA, or the one that it leaves to the next.
 __device__ __forceinline__ uint32_t part_slot(uint32_t c, const Part &t) { return 2 * c + (c == t.c_first ? 1 : 0); }
 
-// One row by one warp, place by place over what it sees and nothing else: for
-// rows whose matrix products met infinities or NaN.  In those a place that the
-// row does not see, but another row of the tile does, has weight 0, and 0
-// times an infinity is NaN; here such a place is never touched.
-template <int DT>
-__device__ __noinline__ void attend_row(const AttnParams &p, const SeqInfo &s, uint32_t seq, uint32_t kvh, uint32_t row) {
-    const uint32_t lane = threadIdx.x & 31, d = p.cache.head_dim;
-    const uint32_t i = div_by(row, p.group), head = kvh * p.group.d + row - i * p.group.d;
-    const Range r = token_range(p, s, i);
-    const int32_t *ids = p.cache.table + uint64_t(seq) * p.cache.table_stride;
-    const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q.p + (s.q0 + i) * p.q.ts + head * p.q.hs);
-    float qv[8], o[8], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t e = lane + 32 * j;
-        qv[j] = e < d ? __uint_as_float(uint32_t(q[e]) << 16) : 0.f;
-        o[j] = 0.f;
-    }
-    auto load = [&](const uint8_t *base, uint32_t e) {
-        if constexpr (DT == SZ_BF16)
-            return __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t *>(base) + e)) << 16);
-        else
-            return __half2float(__ushort_as_half(uint16_t(uint32_t(__ldg(base + e)) << 8)));
-    };
-    for (uint32_t t = r.lo; t < r.hi; ++t) {
-        const uint64_t off = place_offset(p.cache, p.ctl, ids, t);
-        const uint64_t at = off + uint64_t(kvh) * d * (DT == SZ_BF16 ? 2 : 1);
-        float x = 0.f;
-        if (off != kBadOffset) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (lane + 32 * j < d) x = fmaf(qv[j], load(p.cache.k + at, lane + 32 * j), x);
-        }
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-        x *= p.scale_log2;
-        const float mn = fmaxf(m, x), safe = mn == -INFINITY ? 0.f : mn;
-        const float c = exp2_fast(m - safe), e = exp2_fast(x - safe);
-        m = mn;
-        l = l * c + e;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool in = lane + 32 * j < d && off != kBadOffset;
-            o[j] = fmaf(e, in ? load(p.cache.v + at, lane + 32 * j) : 0.f, o[j] * c);
-        }
-    }
-    uint16_t *out = reinterpret_cast<uint16_t *>(p.out.p + (s.q0 + i) * p.out.ts + head * p.out.hs);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (lane + 32 * j < d) out[lane + 32 * j] = uint16_t(pack_bf16(l == 0.f ? 0.f : o[j] / l, 0.f));
+// Values that are not finite.  In the products a place that a row does not see
+// has the weight 0, and 0 times an infinity is NaN.  Only at a tile's edges, the
+// places that some of its rows see and others do not, can a row meet such a
+// place.  There values that are not finite go into the products as 0, and what
+// they add to the rows that see them is added to those rows' sums by itself.  An
+// edge is at most as long as the tile's tokens are many, so this costs little
+// however long the context is (doing a row again, place by place, took 100 ms
+// for 512 tokens over 16,384 places with one NaN among the tokens).
+
+// Places that every row of a tile sees: part of what any of them sees, or, if
+// there are none, [hi, hi) of that.
+__device__ __forceinline__ Range seen_by_all(const AttnParams &p, const Part &t) {
+    const uint32_t hi = token_range(p, t.s, div_by(t.r0, p.group)).hi;
+    const uint32_t lo = token_range(p, t.s, div_by(t.r0 + t.rows - 1, p.group)).lo;
+    return lo < hi ? Range{lo, hi} : Range{t.r.hi, t.r.hi};
 }
 
-// A row whose result is not finite: right as it is unless a place that the row
-// does not see, but another row of its tile does (`tile` is what any of them
-// sees), holds a value that is not finite; then the row is done again by
-// itself.  All lanes of a warp call it.
+// Whether some of [lo, hi), places of the tile, are edges.
+__device__ __forceinline__ bool has_edges(const Range &all, uint32_t lo, uint32_t hi) {
+    return lo < hi && (lo < all.lo || hi > all.hi);
+}
+
+// Bits of kNotFinite are set for values with an exponent of ones only: one step of
+// the exponent more carries to the sign's bit, and no further.
 template <int DT>
-__device__ void repair_row(const AttnParams &p, const SeqInfo &s, uint32_t seq, uint32_t kvh, uint32_t row,
-                           const Range &tile) {
-    const uint32_t lane = threadIdx.x & 31, d = p.cache.head_dim;
-    const Range r = token_range(p, s, div_by(row, p.group));
+constexpr uint32_t kNotFinite = DT == SZ_BF16 ? 0x80008000u : 0x80808080u;
+template <int DT>
+__device__ __forceinline__ uint32_t carries(uint32_t w) {
+    return (w & ~kNotFinite<DT>) + (DT == SZ_BF16 ? 0x00800080u : 0x04040404u);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t carries(const uint4 &v) {
+    return carries<DT>(v.x) | carries<DT>(v.y) | carries<DT>(v.z) | carries<DT>(v.w);
+}
+// 16 bytes of values, with 0 for those that are not finite; says whether there were any.
+template <int DT>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    constexpr uint32_t shift = DT == SZ_BF16 ? 15 : 7;
+    const uint32_t ones = (carries<DT>(w) & kNotFinite<DT>) >> shift;  // 1 in the lowest bit of each such value
+    return w & ~(ones * (DT == SZ_BF16 ? 0xffffu : 0xffu));
+}
+template <int DT>
+__device__ __forceinline__ bool make_finite(uint4 &v) {
+    if ((carries<DT>(v) & kNotFinite<DT>) == 0) return false;
+    v = make_uint4(finite_only<DT>(v.x), finite_only<DT>(v.y), finite_only<DT>(v.z), finite_only<DT>(v.w));
+    return true;
+}
+
+// Adds to N of a row's sums, columns col.., the values that are not finite of the
+// edges among places [from, to) that the row sees.
+template <int DT, int N>
+__device__ __forceinline__ void add_not_finite(const AttnParams &p, uint32_t seq, uint32_t kvh, const Range &row,
+                                               const Range &all, uint32_t from, uint32_t to, uint32_t col, float *sum) {
     const int32_t *ids = p.cache.table + uint64_t(seq) * p.cache.table_stride;
-    auto poisoned = [&](uint32_t lo, uint32_t hi) {
-        bool bad = false;
-        for (uint32_t t = lo; t < hi; ++t) {
-            const uint64_t off = place_offset(p.cache, p.ctl, ids, t);
-            if (off == kBadOffset) continue;
-            const uint8_t *v = p.cache.v + off + uint64_t(kvh) * d * (DT == SZ_BF16 ? 2 : 1);
-            for (uint32_t e = lane; e < d; e += 32) {
-                if constexpr (DT == SZ_BF16)
-                    bad = bad || (reinterpret_cast<const uint16_t *>(v)[e] & 0x7f80u) == 0x7f80u;
-                else
-                    bad = bad || (v[e] & 0x7cu) == 0x7cu;
+    const uint64_t first = uint64_t(kvh) * p.cache.head_dim + col;
+    to = min(to, row.hi);
+#pragma unroll 1
+    for (uint32_t t = max(from, row.lo); t < to; ++t) {
+        if (t >= all.lo && t < all.hi) {
+            t = all.hi - 1;
+            continue;
+        }
+        const uint64_t off = place_offset(p.cache, p.ctl, ids, t);
+        if (off == kBadOffset) continue;
+        if constexpr (DT == SZ_BF16) {
+            const uint2 *at = reinterpret_cast<const uint2 *>(p.cache.v + off + first * 2);
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                const uint2 w = __ldg(at + j / 4);
+                const float v[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!(fabsf(v[e]) < INFINITY)) sum[j + e] += v[e];
+            }
+        } else {
+            const uint32_t *at = reinterpret_cast<const uint32_t *>(p.cache.v + off + first);
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                const uint32_t w = __ldg(at + j / 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = __half2float(__ushort_as_half(uint16_t((w >> (8 * e) & 0xff) << 8)));
+                    if (!(fabsf(v) < INFINITY)) sum[j + e] += v;
+                }
             }
         }
-        return bool(__any_sync(0xffffffffu, bad));
-    };
-    if (poisoned(tile.lo, min(r.lo, tile.hi)) || poisoned(max(r.hi, tile.lo), tile.hi))
-        attend_row<DT>(p, s, seq, kvh, row);
+    }
 }
 
 }  // namespace sz

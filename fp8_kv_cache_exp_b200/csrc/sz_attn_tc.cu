@@ -14,7 +14,8 @@
 //                   then q k' of the next block; the other tile's products run
 //                   while this one's softmax does
 //   warps 14, 15    queries into shared memory: a tile's as soon as its last
-//                   product with the ones before is done
+//                   product with the ones before is done; values that are not
+//                   finite out of the products (sz_attn.cuh)
 // m is the largest score so far only to within 2^SLACK: the sums are rescaled
 // (through registers) when a row's maximum has grown by more, so that most
 // blocks leave them where they are.
@@ -103,25 +104,25 @@ struct TcCfg {
 
 struct TcAux {
     uint64_t full[10], empty[10];
+    uint64_t edge_here[10];  // values of a block with edges have come, to be looked at before they are `full`
     uint64_t raw_full[8], raw_empty[8];
     uint64_t q_full[2], q_empty[2], q_here[2];  // (q_here: E5M2, queries as they come, for the softmax's threads to make fp16)
     uint64_t s_full[2], p_full[2][2];  // a tile's scores; the halves of its weights
     uint64_t o_full[2];                // a tile's sums, at the end of a part
     uint64_t turn[2];                  // a tile's turn at ex2
     uint64_t drain[2];
-    uint32_t tmem, abort, bad;
+    uint32_t tmem, abort;
+    uint32_t edge;  // an edge held a value that is not finite
     uint16_t order[kFewTiles];
 };
 static_assert(sizeof(TcAux) <= 1024, "aux");
 
-// What a CTA leaves for the joining kernel: its share, and the tile of it that
-// it shares with later CTAs only.
+// What a CTA leaves for the joining kernel: the tile that it shares with later
+// CTAs only.
 struct TcDesc {
-    Work begin, join;
-    uint32_t bad;    // rows of its own tiles came out not finite
-    uint32_t joins;  // `join` is one
-    uint32_t has, pad;
-    uint16_t order[kFewTiles];
+    Work join;
+    uint32_t joins;  // there is one
+    uint32_t pad;
 };
 static_assert(sizeof(TcDesc) * kMaxSms <= kDescBytes, "descriptors");
 
@@ -183,9 +184,6 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void sts_u128(uint32_t a, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // ------------------------------------------------------------ tensor memory
@@ -349,6 +347,24 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
         const int32_t *ids = p.cache.table + uint64_t(w.seq) * p.cache.table_stride;
         const uint32_t part_hi = min((t.block0 + t.to) * kTcBlock, t.r.hi);
         const uint64_t head_off = uint64_t(w.head) * d * C::EB + piece * 16;
+        const Range all = seen_by_all(p, t);
+        // Whether block j has edges.
+        auto edges = [&](uint32_t j) {
+            const uint32_t at = (t.block0 + j) * kTcBlock;
+            return has_edges(all, max(at, t.r.lo), min(at + kTcBlock, part_hi));
+        };
+        auto is_edge = [&](uint32_t j, uint32_t row) {
+            const uint32_t at = (t.block0 + j) * kTcBlock + row;
+            return at < all.lo || at >= all.hi;
+        };
+        // The u-th piece of block j's edges that this thread has copied.
+        auto clean = [&](uint32_t j, uint32_t u, uint4 &v) {
+            if (is_edge(j, row0 + u * ROWS) && make_finite<DT>(v)) {
+                *reinterpret_cast<volatile uint32_t *>(&aux->edge) = 1;
+                return true;
+            }
+            return false;
+        };
 
         // the place of this lane's row of a block, and its page's id
         auto place = [&](uint32_t j) { return (t.block0 + j) * kTcBlock + warp * 32 + lane; };
@@ -439,8 +455,10 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
             if constexpr (DT == SZ_BF16) {
                 for (uint32_t n = 0; n < tiles; ++n, ++issued) {
                     if (!wait_free(issued)) return;
+                    // (the query warps look at edges)
+                    const bool edge = (n & 1) && edges(t.from + n / 2);
                     next_fetch(n, base + C::RING_AT + (issued % C::STAGES) * C::STAGE, C::STAGE,
-                               &aux->full[issued % C::STAGES]);
+                               edge ? &aux->edge_here[issued % C::STAGES] : &aux->full[issued % C::STAGES]);
                 }
                 ready = issued;
             } else {
@@ -456,12 +474,18 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
                     const uint32_t x = raw0 + n + 1 - C::RAWS, slot = x % C::RAWS;
                     if (!warp_wait(&aux->raw_full[slot], (x / C::RAWS) & 1, aux, p) || !wait_free(issued)) return;
                     if (has_piece) {
+                        const uint32_t m = x - raw0, j = t.from + m / 2;
+                        const bool edge = (m & 1) && edges(j);
 #pragma unroll
                         for (uint32_t u0 = 0; u0 < N; u0 += 4) {
                             uint4 v[4];
 #pragma unroll
                             for (uint32_t u = 0; u < 4; ++u)
                                 v[u] = lds_u128(base + C::RAW_AT + slot * C::RAW + (row0 + (u0 + u) * ROWS) * DP + piece * 16);
+                            if (edge) {
+#pragma unroll
+                                for (uint32_t u = 0; u < 4; ++u) clean(j, u0 + u, v[u]);
+                            }
 #pragma unroll
                             for (uint32_t u = 0; u < 4; ++u)
                                 spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + (u0 + u) * ROWS, piece, v[u]);
@@ -485,23 +509,37 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
             copy((n & 1) ? p.cache.v : p.cache.k, off, to);
         };
         if constexpr (DT == SZ_BF16) {
+            const uint32_t first = issued;
+            auto at = [&](uint32_t stage, uint32_t u) {
+                const uint32_t row = row0 + u * ROWS;
+                return base + C::RING_AT + (stage % C::STAGES) * C::STAGE + (piece / 8) * kPanel + row * 128 +
+                       (((piece % 8) ^ (row & 7)) << 4);
+            };
+            auto arrived = [&](uint32_t to) {
+                for (uint32_t x = ready; x < to; ++x) {
+                    const uint32_t n = x - first;
+                    if (!(n & 1) || !has_piece || !edges(t.from + n / 2)) continue;
+#pragma unroll 1
+                    for (uint32_t u = 0; u < N; ++u) {
+                        uint4 v = lds_u128(at(x, u));
+                        if (clean(t.from + n / 2, u, v)) sts_u128(at(x, u), v);
+                    }
+                }
+                hand_over(to);
+            };
             for (uint32_t n = 0; n < tiles; ++n) {
                 if (!stage_free(issued)) {
                     cp_wait<0>();
-                    hand_over(issued);
+                    arrived(issued);
                     if (!wait_free(issued)) return;
                 }
-                const uint32_t dst = base + C::RING_AT + (issued % C::STAGES) * C::STAGE + (piece / 8) * kPanel;
-                next_copy(n, [&](uint32_t u) {
-                    const uint32_t row = row0 + u * ROWS;
-                    return dst + row * 128 + (((piece % 8) ^ (row & 7)) << 4);
-                });
+                next_copy(n, [&](uint32_t u) { return at(issued, u); });
                 ++issued;
                 cp_wait<2>();
-                if (issued > ready + 2) hand_over(issued - 2);
+                if (issued > ready + 2) arrived(issued - 2);
             }
             cp_wait<0>();
-            hand_over(issued);
+            arrived(issued);
         } else {
             const uint32_t raw = base + C::RAW_AT + tid * 16;
             constexpr uint32_t LAG = 2;  // tiles under way behind the one that is spread
@@ -511,6 +549,7 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
                 if (n < LAG) continue;
                 const uint32_t m = n - LAG;  // the tile that has come
                 cp_wait<LAG>();
+                const bool edge = (m & 1) && edges(t.from + m / 2);
                 if (!wait_free(issued)) return;
                 if (has_piece) {
 #pragma unroll
@@ -518,6 +557,10 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
                         uint4 v[4];
 #pragma unroll
                         for (uint32_t u = 0; u < 4; ++u) v[u] = lds_u128(raw + (m % C::RAWS) * C::RAW + (u0 + u) * 2048);
+                        if (edge) {
+#pragma unroll
+                            for (uint32_t u = 0; u < 4; ++u) clean(t.from + m / 2, u0 + u, v[u]);
+                        }
 #pragma unroll
                         for (uint32_t u = 0; u < 4; ++u)
                             spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + (u0 + u) * ROWS, piece, v[u]);
@@ -547,16 +590,22 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
 
 // Queries into shared memory (warps 14, 15): by tensor copies of 128 / G tokens
 // of the group's G heads where G divides 128 (`map`; rows behind the sequence's
-// last are then the next one's, and nobody's), or row by row.
+// last are then the next one's, and nobody's), or row by row.  Behind a part's
+// queries the warps look at the values of its edges, where these come by tensor
+// copies in the products' layout (`edges`): nobody has had those in registers.
+// (Two 1024-token prompts of 32 heads of 80, and 2048 tokens over 8192 places:
+// 39 and 227 us; by the load warps 43 and 265; by one warp beside the queries 47
+// and 228; not at all 36 and 223.)
 constexpr uint32_t kQueryWarps = 2;
 template <int DT, int DP>
-__device__ __forceinline__ void query_parts(const AttnParams &p, const CUtensorMap *map, Work w, uint32_t base, TcAux *aux,
-                                            uint32_t &seen, uint32_t &phases) {
+__device__ __forceinline__ void query_parts(const AttnParams &p, const CUtensorMap *map, bool edges, Work w, uint32_t base,
+                                            TcAux *aux, uint32_t &seen, uint32_t &phases) {
     using C = TcCfg<DT, DP>;
     constexpr uint32_t QL = DP / 8, QR = 32 / QL;          // lanes to a row, rows to an instruction
     constexpr uint32_t BATCH = 8;
     const uint32_t lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 14, c = lane % QL;
     const uint32_t d = p.cache.head_dim, G = p.group.d;
+    uint32_t kv = 0, edge_phases = 0;  // the part's first stage; bit i: the phase of edge_here[i]
     for (;;) {
         const Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, blockIdx.x);
         const uint8_t *q = p.q.p + uint64_t(t.s.q0) * p.q.ts + uint64_t(w.head * G) * p.q.hs;
@@ -608,15 +657,46 @@ __device__ __forceinline__ void query_parts(const AttnParams &p, const CUtensorM
             bar_arrive(bar);
             __syncwarp();
         }
+        if (DT == SZ_BF16 && edges) {
+            const Range all = seen_by_all(p, t);
+            for (uint32_t j = t.from; j < t.to; ++j) {
+                const uint32_t at = (t.block0 + j) * kTcBlock, lo = max(at, t.r.lo), hi = min(at + kTcBlock, t.r.hi);
+                if (!has_edges(all, lo, hi)) continue;
+                const uint32_t stage = (kv + 2 * (j - t.from) + 1) % C::STAGES;
+                if (!warp_wait(&aux->edge_here[stage], (edge_phases >> stage) & 1, aux, p)) return;
+                edge_phases ^= 1u << stage;
+                const uint32_t block = base + C::RING_AT + stage * C::STAGE + (c / 8) * kPanel;
+                auto look = [&](uint32_t from, uint32_t to) {
+                    from += warp * QR + lane / QL;
+                    auto address = [&](uint32_t x) { return block + (x - at) * 128 + (((c % 8) ^ (x & 7)) << 4); };
+                    uint32_t found = 0;
+#pragma unroll 8
+                    for (uint32_t x = from; x < to; x += kQueryWarps * QR) found |= carries<DT>(lds_u128(address(x)));
+                    if ((found & kNotFinite<DT>) == 0) return;
+                    *reinterpret_cast<volatile uint32_t *>(&aux->edge) = 1;
+                    for (uint32_t x = from; x < to; x += kQueryWarps * QR) {
+                        uint4 v = lds_u128(address(x));
+                        if (make_finite<DT>(v)) sts_u128(address(x), v);
+                    }
+                };
+                look(lo, min(hi, all.lo));
+                look(max(lo, all.hi), hi);
+                fence_proxy_async_smem();
+                // (`full` counts the 128 threads of the load warps)
+                for (uint32_t x = 0; x < 128 / (32 * kQueryWarps); ++x) bar_arrive(&aux->full[stage]);
+                __syncwarp();
+            }
+            kv += 2 * (t.to - t.from);
+        }
         if (!work_next<kTcRows, kTcExtra>(p, w, t, aux->order)) return;
     }
 }
 
 template <int DT, int DP>
-__device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMap *map, const Work &w, uint32_t base,
-                                           TcAux *aux) {
+__device__ __forceinline__ void query_role(const AttnParams &p, const CUtensorMap *map, bool edges, const Work &w,
+                                           uint32_t base, TcAux *aux) {
     uint32_t seen = 0, phases = 0;  // bit i: tile i has been there; the phase of q_empty[i], and of the last copy
-    query_parts<DT, DP>(p, map, w, base, aux, seen, phases);
+    query_parts<DT, DP>(p, map, edges, w, base, aux, seen, phases);
     cp_wait<0>();
     if (!map || threadIdx.x / 32 != 14) return;
     uint64_t *here = DT == SZ_BF16 ? aux->q_full : aux->q_here;
@@ -724,8 +804,7 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Work w, uint32_t b
 // A warp's 32 rows of a tile with few parts: the warp that comes last to them
 // adds them up, in the parts' order.
 template <int DT>
-__device__ __forceinline__ void join_few(const AttnParams &p, const Work &w, const Part &t, uint32_t r, uint32_t parts,
-                                         TcAux *aux) {
+__device__ __forceinline__ void join_few(const AttnParams &p, const Work &w, const Part &t, uint32_t r, uint32_t parts) {
     constexpr float RAISE = TcCfg<DT, 64>::RAISE;
     const uint32_t d = p.cache.head_dim, lane = threadIdx.x & 31;
     uint32_t *arrived = p.arrived + t.c_first * 8 + r / 32;
@@ -753,7 +832,6 @@ __device__ __forceinline__ void join_few(const AttnParams &p, const Work &w, con
     const float inv = L == 0.f ? 0.f : 1.f / L;
     uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs;
     const bool aligned32 = ((reinterpret_cast<uintptr_t>(p.out.p) | p.out.ts | p.out.hs) & 31) == 0;
-    float worst = 0.f;
     for (uint32_t e = 0; e < d; e += 16) {
         float v[16];
 #pragma unroll
@@ -772,18 +850,14 @@ __device__ __forceinline__ void join_few(const AttnParams &p, const Work &w, con
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             v[2 * j] *= inv, v[2 * j + 1] *= inv;
-            worst = fmaf(0.f, v[2 * j], fmaf(0.f, v[2 * j + 1], worst));  // stays 0, or is NaN
             pk[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
         }
         if (r < t.rows) {
             store32(out + 2 * e, pk, aligned32);
         }
     }
-    if (r < t.rows) {
-        if (p.lse)
-            p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] = L == 0.f ? -INFINITY : kLn2 * (M - RAISE + log2f(L));
-        if (worst != 0.f) aux->bad = 1;
-    }
+    if (r < t.rows && p.lse)
+        p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] = L == 0.f ? -INFINITY : kLn2 * (M - RAISE + log2f(L));
 }
 
 // Softmax of one tile's rows, a thread a row, and what becomes of the sums.
@@ -961,12 +1035,32 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
             look_ahead();
             if (!warp_wait(&aux->o_full[i], o_uses++ & 1, aux, p)) return;
             tc_after();
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(&aux->edge) != 0)) {
+                // values that are not finite, which the products went without
+                const Range all = seen_by_all(p, t);
+                const uint32_t from = (t.block0 + t.from) * kTcBlock, to = min((t.block0 + t.to) * kTcBlock, t.r.hi);
+#pragma unroll 1
+                for (uint32_t k = 0; k < d; k += 16) {
+                    uint32_t o[16];
+                    float sum[16];
+                    tc_ld16(o, o_at + k);
+                    tc_wait_ld();
+                    tc_arrived(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[e] = __uint_as_float(o[e]);
+                    add_not_finite<DT, 16>(p, w.seq, w.head, rr, all, from, to, k, sum);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(sum[e]);
+                    __syncwarp();
+                    tc_st16(o_at + k, o);
+                }
+                tc_wait_st();
+            }
             if (whole_tile) {
                 const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
                 const float f = l == 0.f ? 0.f : 1.f / l;
                 uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs;
                 const bool aligned32 = ((reinterpret_cast<uintptr_t>(p.out.p) | p.out.ts | p.out.hs) & 31) == 0;
-                float worst = 0.f;
                 for (uint32_t k = 0; k < d; k += 16) {
                     uint32_t o[16];
                     tc_ld16(o, o_at + k);
@@ -975,19 +1069,15 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float a = __uint_as_float(o[2 * e]) * f, b = __uint_as_float(o[2 * e + 1]) * f;
-                        worst = fmaf(0.f, a, fmaf(0.f, b, worst));  // stays 0, or is NaN
                         pk[e] = pack_bf16(a, b);
                     }
                     if (r < t.rows) {
                         store32(out + 2 * k, pk, aligned32);
                     }
                 }
-                if (r < t.rows) {
-                    if (p.lse)
-                        p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] =
-                            l == 0.f ? -INFINITY : kLn2 * (m - C::RAISE + log2f(l));
-                    if (worst != 0.f) aux->bad = 1;
-                }
+                if (r < t.rows && p.lse)
+                    p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] =
+                        l == 0.f ? -INFINITY : kLn2 * (m - C::RAISE + log2f(l));
             } else {
                 // four columns of 256 rows at a time, then the rows' m and l
                 float *part = p.part + uint64_t(part_slot(blockIdx.x, t)) * kTcRows * (d + 2) + r;
@@ -1003,7 +1093,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
                 }
                 part[d * kTcRows] = m;
                 part[(d + 1) * kTcRows] = l;
-                if (parts <= kFewParts) join_few<DT>(p, w, t, r, parts, aux);
+                if (parts <= kFewParts) join_few<DT>(p, w, t, r, parts);
             }
             // the sums are read before the next part's first weights are announced
             tc_before();
@@ -1033,6 +1123,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (uint32_t i = 0; i < C::STAGES; ++i) {
             mbar_init(&aux->full[i], 128);
             mbar_init(&aux->empty[i], 2);
+            mbar_init(&aux->edge_here[i], 128);
         }
         for (int i = 0; i < int(C::RAWS); ++i) {
             mbar_init(&aux->raw_full[i], 128);
@@ -1051,20 +1142,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(&aux->drain[1], 1);
         fence_mbar_init();
         aux->abort = 0;
-        aux->bad = 0;
+        aux->edge = 0;
     }
     pdl_wait();
     pdl_launch_dependents();
     Work w;
     const bool has = work_begin<kTcThreads, kTcRows, kTcBlock, kTcExtra>(
         p, *reinterpret_cast<WorkScratch<kTcThreads> *>(smem + C::RING_AT), w, aux->order);
-    if (tid == 0) {
-        desc->joins = 0;
-        desc->has = has;
-        desc->bad = 0;
-        if (has) desc->begin = w;
-    }
-    if (has && tid < kFewTiles) desc->order[tid] = w.whole ? aux->order[tid] : 0;
+    if (tid == 0) desc->joins = 0;
     if (!has) return;
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&aux->tmem))
@@ -1097,14 +1182,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_wait(&aux->drain[warp - 12], 0, kLandLimitNs);
             __syncwarp();
         } else {
-            query_role<DT, DP>(p, q_box ? &q_map : nullptr, w, base, aux);
+            query_role<DT, DP>(p, q_box ? &q_map : nullptr, box > 0, w, base, aux);
         }
     }
     __syncwarp();
     tc_before();
     __syncthreads();
     tc_after();
-    if (tid == 0 && aux->bad) desc->bad = 1;
     if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -1125,7 +1209,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     constexpr uint32_t COLS = DP / kJoinSplit;
     __shared__ float s_o[kJoinGroups - 1][DP][kJoinRows];
     __shared__ float s_m[kJoinWarps][kJoinRows], s_l[kJoinWarps][kJoinRows];
-    __shared__ uint32_t s_bad;
     pdl_wait();
     pdl_launch_dependents();
     __shared__ uint32_t s_list[kJoinWarps][33];
@@ -1134,7 +1217,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const TcDesc *descs = reinterpret_cast<const TcDesc *>(p.desc);
     // the tiles to join, listed by each warp for its 32 of the CTAs
     {
-        const bool joins = threadIdx.x < gridDim.x && descs[threadIdx.x].has && descs[threadIdx.x].joins;
+        const bool joins = threadIdx.x < gridDim.x && descs[threadIdx.x].joins;
         const uint32_t all = __ballot_sync(0xffffffffu, joins);
         if (joins) s_list[warp][1 + __popc(all & lanemask_lt())] = threadIdx.x;
         if (lane == 0) s_list[warp][0] = __popc(all);
@@ -1153,7 +1236,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         if (slice * kJoinRows < t.rows) {
             __syncthreads();  // (the last item's sums are read)
             const uint32_t r = slice * kJoinRows + lane, parts = t.c_last - t.c_first + 1;
-            if (threadIdx.x == 0) s_bad = 0;
             auto slot = [&](uint32_t k) {
                 return p.part + uint64_t(part_slot(t.c_first + k, t)) * kTcRows * (d + 2) + r;
             };
@@ -1197,7 +1279,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
                 for (uint32_t k = 0; k < kJoinWarps; ++k) L += s_l[k][lane];
                 const float inv = L == 0.f ? 0.f : 1.f / L;
                 uint8_t *out = p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs + 2 * col0;
-                float worst = 0.f;
 #pragma unroll
                 for (uint32_t e = 0; e < COLS; e += 4) {
                     if (e >= d / kJoinSplit) break;
@@ -1206,7 +1287,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 #pragma unroll
                         for (uint32_t k = 0; k < kJoinGroups - 1; ++k) v[j] += s_o[k][col0 + j][lane];
                         v[j] *= inv;
-                        worst = fmaf(0.f, v[j], worst);  // stays 0, or is NaN
                     }
                     if (r < t.rows)
                         *reinterpret_cast<uint2 *>(out + 2 * e) =
@@ -1215,33 +1295,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
                 if (warp == 0 && r < t.rows && p.lse)
                     p.lse[uint64_t(t.s.q0 + tok) * p.q.heads + head] =
                         L == 0.f ? -INFINITY : kLn2 * (M - C::RAISE + log2f(L));
-                if (r < t.rows && worst != 0.f) atomicOr(&s_bad, 1u << lane);
             }
-            __syncthreads();
-            uint32_t k = 0;
-            for (uint32_t bad = s_bad; bad; bad &= bad - 1, ++k) {
-                const uint32_t x = __ffs(bad) - 1;
-                if (k % kJoinWarps == warp)
-                    repair_row<DT>(p, t.s, w.seq, w.head, t.r0 + slice * kJoinRows + x, t.r);
-            }
-        }
-    }
-    const uint32_t c = blockIdx.x;
-    if (descs[c].has && descs[c].bad) {
-        // rows that are not finite of the tiles that the CTA had alone, or joined
-        Work w = descs[c].begin;
-        for (;;) {
-            const Part t = work_part<kTcRows, kTcBlock, kTcExtra>(p, w, c);
-            if (t.c_last - t.c_first < kFewParts)
-                for (uint32_t r = warp; r < t.rows; r += kJoinWarps) {
-                    const uint32_t g = t.r0 + r, tok = div_by(g, p.group), head = w.head * G + (g - tok * G);
-                    const uint16_t *out = reinterpret_cast<const uint16_t *>(
-                        p.out.p + uint64_t(t.s.q0 + tok) * p.out.ts + uint64_t(head) * p.out.hs);
-                    bool bad = false;
-                    for (uint32_t e = lane; e < d; e += 32) bad = bad || (out[e] & 0x7f80u) == 0x7f80u;
-                    if (__any_sync(0xffffffffu, bad)) repair_row<DT>(p, t.s, w.seq, w.head, g, t.r);
-                }
-            if (!work_next<kTcRows, kTcExtra>(p, w, t, descs[c].order)) break;
         }
     }
 }
