@@ -917,7 +917,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
                     sts_u128(chunk(c + 1), make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
                                                       pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up)));
                 }
-                sc *= __uint_as_float(uint32_t(127 - e) << 23);
+                // (not 0, which times a masked score's -infinity is NaN; scores times 2^-126 are below 2^-80, as they are times less)
+                sc = fmaxf(sc * __uint_as_float(uint32_t(127 - e) << 23), 1.17549435e-38f);
                 fence_proxy_async_smem();
                 bar_arrive(&aux->q_full[i]);
             }

@@ -7,7 +7,7 @@ import torch
 
 import paged_ops as P
 from gpu_helpers import sz
-from test_gpu_paged_ops import BF16, E5M2, close, gen, run_attention
+from test_gpu_paged_ops import BF16, E5M2, check_attention, close, gen, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,10 @@ def test_values_that_are_not_finite_cost_no_more_than_others(dtype, q_len, all_t
     assert torch.isnan(out[-1]).all() and torch.isnan(out[0]).all() == all_tokens
     print("%.3f ms, and %.3f without NaN" % (spoiled, clean))
     assert spoiled < 4 * clean + 0.2, "%.3f ms, and %.3f without NaN" % (spoiled, clean)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("q_lens,kv_lens,window", [([100, 70], [300, 70], 0), ([90], [500], 33), ([2, 1], [90, 30], 0)])
+def test_scores_that_vanish(dtype, q_lens, kv_lens, window):
+    """Queries near the smallest numbers and a small scale: every place that a row sees weighs the same."""
+    check_attention(sz(), dtype, q_lens, kv_lens, 4, 2, 64, 16, window=window, scale=2.0 ** -40, spread=2.0 ** -115, seed=44)
