@@ -4,12 +4,14 @@ KV-cache tensors on a B200 GPU (SplitZip project page, Abstract and FAQ).
 Argument marshalling only: the functions below have the names of the C ABI in
 include/splitzip.h and pass torch tensors' device pointers and the current CUDA
 stream to it.  Every step of the codec runs in the library's CUDA kernels.
-Importing this package loads libsplitzip.so and _host.so and raises ImportError if they
-have not been built (python fp8_kv_cache_exp_b200/build.py); there is no other path.
+Importing this package loads libsplitzip.so and raises ImportError if it has not been built
+(python fp8_kv_cache_exp_b200/build.py); there is no other path.  The operators on a paged
+cache load _host.*.so, built for this Python and torch, at their first call, in the same way.
 """
 import ctypes
 import os
 import struct
+import threading
 
 import torch
 
@@ -103,12 +105,26 @@ def _load():
 lib = _load()
 
 
+class _Host:
+    """In place of the module _host until its first use: the codec needs neither it nor torch's layouts."""
+    _lock = threading.Lock()
+
+    def __getattr__(self, name):
+        global _host
+        with self._lock:
+            if _host is self:
+                _host = _load_host()
+        return getattr(_host, name)
+
+
 def _load_host():
-    path = os.path.join(os.path.dirname(lib_path), "_host.so")
-    if not os.path.exists(path):
-        raise ImportError("_host.so is not built (%s); run: python fp8_kv_cache_exp_b200/build.py" % path)
     from importlib.machinery import ExtensionFileLoader
     from importlib.util import module_from_spec, spec_from_loader
+
+    from .build import host_path
+    path = host_path()
+    if not os.path.exists(path):
+        raise ImportError("%s is not built; run: python fp8_kv_cache_exp_b200/build.py" % path)
     loader = ExtensionFileLoader(__name__ + "._host", path)
     host = module_from_spec(spec_from_loader(loader.name, loader))
     loader.exec_module(host)
@@ -118,7 +134,7 @@ def _load_host():
     return host
 
 
-_host = _load_host()
+_host = _Host()
 
 
 class SplitZipError(RuntimeError):

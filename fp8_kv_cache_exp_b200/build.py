@@ -1,5 +1,6 @@
 """Build libsplitzip.so (the CUDA library behind the C ABI) in-tree for sm_100a,
-and _host (the Python binding's argument checks of the paged-cache operators).
+and _host.*.so (the Python binding's argument checks of the paged-cache operators),
+whose name says which Python and torch it is for.
 
 Usage: python fp8_kv_cache_exp_b200/build.py [--force]
 (run it by path: importing the package itself loads the library it builds)
@@ -15,7 +16,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsplitzip.so")
-HOST = os.path.join(HERE, "_host.so")
 HOST_SRC = os.path.join(CSRC, "sz_host.cpp")
 
 NVCC_FLAGS = [
@@ -43,21 +43,30 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def host_path() -> str:
+    """The binding's module for this interpreter and its torch, whose tensors it reads by their layout."""
+    import sysconfig
+    import torch
+    return os.path.join(HERE, "_host.torch-%s%s" % (torch.__version__, sysconfig.get_config_var("EXT_SUFFIX")))
+
+
 def host_up_to_date() -> bool:
-    return os.path.exists(HOST) and all(os.path.getmtime(p) <= os.path.getmtime(HOST)
+    host = host_path()
+    return os.path.exists(host) and all(os.path.getmtime(p) <= os.path.getmtime(host)
                                         for p in (HOST_SRC, os.path.join(INCLUDE, "splitzip.h")))
 
 
 def build_host(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/sz_host.cpp against this interpreter and its torch."""
+    host = host_path()
     if not force and host_up_to_date():
-        return HOST
+        return host
     import sysconfig
     import torch
     at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(os.environ.get("NVCC", "nvcc")) or
                                                             "/usr/local/cuda/bin/nvcc")))
-    tmp = HOST + ".tmp.%d" % os.getpid()
+    tmp = host + ".tmp.%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
            "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(at, "include"),
@@ -67,17 +76,22 @@ def build_host(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
-    os.replace(tmp, HOST)
-    return HOST
+    os.replace(tmp, host)
+    return host
 
 
 def build(force: bool = False, extra_flags=(), out: str = LIB, verbose: bool = False, files=None) -> str:
     """Compile every csrc/*.cu, or the named ones (one nvcc per file, in parallel), and link them
-    into one shared library; return its path."""
+    into one shared library; return its path.  Behind the library itself comes the binding's module,
+    which is all that needs torch's headers."""
+    if force or out != LIB or not up_to_date():
+        build_library(extra_flags, out, verbose, files)
     if out == LIB:
         build_host(force, verbose)
-    if not force and out == LIB and up_to_date():
-        return out
+    return out
+
+
+def build_library(extra_flags, out: str, verbose: bool, files) -> None:
     import tempfile
     from concurrent.futures import ThreadPoolExecutor
     nvcc = os.environ.get("NVCC", "nvcc")
@@ -98,7 +112,6 @@ def build(force: bool = False, extra_flags=(), out: str = LIB, verbose: bool = F
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
     os.replace(tmp, out)
-    return out
 
 
 if __name__ == "__main__":
