@@ -145,6 +145,17 @@ struct NormRope {
     }
 };
 
+// The library's call, which waits while the stream's queue of launches is full:
+// other Python threads run meanwhile, as in a call through ctypes.  (The caller
+// holds its tensors and the cache's struct.)
+template <typename F, typename... Args>
+sz_status unlocked(F call, Args... args) {
+    PyThreadState *state = PyEval_SaveThread();
+    const sz_status s = call(args...);
+    PyEval_RestoreThread(state);
+    return s;
+}
+
 template <typename F>
 PyObject *guarded(Py_ssize_t have, Py_ssize_t want, F &&f) {
     if (have != want) {
@@ -187,7 +198,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         nr.fill(s.norm, s.rope, dim, tokens, a[11], a[14]);
         size_t bytes;
         void *w = workspace(ws, &bytes);
-        return g_append(c, &s, w, bytes, stream(a[15], dev.index));
+        return unlocked(g_append, c, &s, w, bytes, stream(a[15], dev.index));
     });
 }
 
@@ -216,7 +227,7 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         s.head_dim = uint32_t(dim);
         size_t bytes;
         void *w = workspace(ws, &bytes);
-        return g_norm_rope(&s, w, bytes, stream(a[11], dev.index));
+        return unlocked(g_norm_rope, &s, w, bytes, stream(a[11], dev.index));
     });
 }
 
@@ -242,7 +253,7 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
         s.window = uint32_t(whole(a[9], "window", 0x7fffffff));
         size_t bytes;
         void *w = workspace(ws, &bytes);
-        return g_attn(c, &s, w, bytes, stream(a[11], dev.index));
+        return unlocked(g_attn, c, &s, w, bytes, stream(a[11], dev.index));
     });
 }
 
