@@ -215,8 +215,18 @@ def sz_max_compressed_size(dtype: int, n: int) -> int:
 
 def new_workspace(dtype: int, ns, device="cuda", stream=None) -> torch.Tensor:
     """A zero-initialised workspace for a batch with element counts ns."""
-    ws = torch.empty(sz_workspace_bytes_batched(dtype, ns), dtype=torch.uint8, device=device)
-    sz_workspace_init(ws, stream)
+    return _zeroed(sz_workspace_bytes_batched(dtype, ns), device, stream)
+
+
+def _zeroed(n: int, device, stream) -> torch.Tensor:
+    """n zero bytes, zeroed on `stream`.  The memory comes from the current stream, whose earlier work may
+    still write to it."""
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+            ws.record_stream(stream)
+        sz_workspace_init(ws, stream)
     return ws
 
 
@@ -562,10 +572,7 @@ def new_ops_workspace(cache: KVCache = None, device=None, stream=None) -> torch.
         raise SplitZipError(SZ_ERR_INVALID_ARG, "sz_ops_workspace_bytes")
     if device is None:
         device = "cuda" if cache is None else cache.k_pool.device
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    with torch.cuda.device(ws.device):
-        sz_workspace_init(ws, stream)
-    return ws
+    return _zeroed(n, device, stream)
 
 
 def rope_table(positions: int, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:

@@ -43,3 +43,25 @@ def test_other_threads_run_during_a_call():
         other.join()
     assert end - begin > 0.9
     assert sum(begin + 0.1 < t < end - 0.1 for t in ticks) > 20
+
+
+@pytest.mark.parametrize("operators", [True, False])
+def test_a_workspace_zeroed_on_another_stream(operators):
+    """Memory that work of the current stream still writes to is zeroed behind that work."""
+    m = sz()
+    c = P.build_cache(gen(51), BF16, [40], 16, 2, 64)
+    cache = m.KVCache(c.k_pool, c.v_pool, c.table)
+    ns = [1 << 24] * 4
+    s = torch.cuda.Stream()
+    n = m.sz_ops_workspace_bytes(cache) if operators else m.sz_workspace_bytes_batched(m.SZ_BF16, ns)
+    old = torch.empty(n, dtype=torch.uint8, device="cuda")
+    address = old.data_ptr()
+    old.fill_(1), m.new_ops_workspace(stream=s)      # (first calls wait for the device)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                   # some 50 ms
+    old.fill_(255)
+    del old
+    ws = m.new_ops_workspace(cache, stream=s) if operators else m.new_workspace(m.SZ_BF16, ns, stream=s)
+    assert ws.data_ptr() == address
+    torch.cuda.synchronize()
+    assert not ws.any()
