@@ -518,8 +518,8 @@ class KVCache:
     """A paged KV cache: k_pool and v_pool [pages, page_tokens, kv_heads, head_dim], bfloat16 or
     float8_e5m2, contiguous inside a page and with the same stride from page to page; table [seqs,
     table_pages] int32, a row the page ids of one sequence in token order.  A row is also the `pages`
-    of paged() with page_elems = page_tokens * kv_heads * head_dim, so a sequence can be coded where it
-    lies.  The tensors must stay alive and in place while the cache is in use (the object holds them);
+    of paged() with page_elems = page_tokens * kv_heads * head_dim: where that is a size the codec takes
+    (a multiple of 1024, at most 2^18), a sequence can be coded where it lies.  The tensors must stay alive and in place while the cache is in use (the object holds them);
     their contents may change between calls."""
 
     def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor, table: torch.Tensor):
@@ -552,6 +552,10 @@ class KVCache:
         """(paged() descriptors of the keys and the values, their element count) of a sequence's first
         `tokens` tokens, for the paged calls of the codec."""
         pe = self.page_tokens * self.kv_heads * self.head_dim
+        if pe % 1024 or pe > 1 << 18:
+            raise ValueError("the codec's pages are a multiple of 1024 elements and at most 2^18; these are %d" % pe)
+        if not 0 <= tokens <= self.table.shape[1] * self.page_tokens:
+            raise ValueError("%d tokens: the table has room for %d" % (tokens, self.table.shape[1] * self.page_tokens))
         out = []
         for pool in (self.k_pool, self.v_pool):
             d = sz_paged_t(pool.data_ptr(), self.table[seq].data_ptr(), pool.shape[0],

@@ -329,8 +329,9 @@ sz_status sz_encode_noalloc(sz_dtype dtype, const sz_plan_t *d_plan, const void 
  * them (sz_attn_paged), and, for caches that are kept contiguous, normalise
  * and rotate queries and keys (sz_qk_norm_rope).  The pages are those of
  * sz_paged_t: a row of `table` is a descriptor's `pages`, and its page_elems is
- * page_tokens * kv_heads * head_dim, so a sequence's keys or values can be
- * coded where they lie.
+ * page_tokens * kv_heads * head_dim; where that is a multiple of 1024 and at
+ * most 2^18, as the codec wants, a sequence's keys or values can be coded where
+ * they lie.  The operators take other pages too.
  *
  * Queries, keys, values and outputs are BF16; the cache is BF16 or E5M2.
  * Arithmetic is in 32 bits, rounded once to the type that is written (to

@@ -61,3 +61,27 @@ def test_the_library_comes_before_the_module(monkeypatch):
 def test_the_module_is_loaded_once():
     assert sz._host.append is sz._host.append
     assert type(sz._host).__name__ == "module"
+
+
+def cache(page, heads, dim, seqs=2, width=4):
+    k = torch.zeros(6, page, heads, dim, dtype=torch.bfloat16)
+    return sz.KVCache(k, k.clone(), torch.zeros(seqs, width, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("page,heads,dim", [(13, 4, 128), (13, 32, 80), (1, 1, 16), (1 << 12, 1, 128)])
+def test_pages_that_the_codec_does_not_take_are_refused(page, heads, dim):
+    c = cache(page, heads, dim)
+    assert sz.sz_ops_workspace_bytes(c) > 0          # (the operators do)
+    with pytest.raises(ValueError, match="1024"):
+        c.pages(0, 1)
+
+
+def test_descriptors_of_a_sequences_pages():
+    c = cache(16, 2, 64)
+    (k, v), n = c.pages(1, 50)
+    assert n == 50 * 128 and k.page_elems == v.page_elems == 2048 and k.pool_pages == 6
+    assert k.pages == c.table[1].data_ptr() and k.pool == c.k_pool.data_ptr() and v.pool == c.v_pool.data_ptr()
+    assert c.pages(0, 64)[1] == 64 * 128 and c.pages(0, 0)[1] == 0
+    for tokens in (65, -1):
+        with pytest.raises(ValueError):
+            c.pages(0, tokens)
