@@ -90,6 +90,11 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Weights in the 16 bits that the tensor cores multiply: of at most 1 (or 2^SLACK
+// behind a maximum that lags), each off by half a step, 2^-8 in bf16 and 2^-11 in
+// fp16, of itself.  The tensor cores take no factors of 32 bits (tf32
+// has fp16's 11, at half the rate), and the output is rounded to bf16.  Sums of
+// weights are taken before the rounding.
 template <int DT>
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
     return DT == SZ_BF16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);

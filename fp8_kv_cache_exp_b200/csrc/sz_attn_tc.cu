@@ -1000,6 +1000,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
                 }
                 const float shift = C::RAISE - (m == -INFINITY ? 0.f : m);
                 const uint64_t sc2 = f2(sc, sc), shift2 = f2(shift, shift);
+                // (the weights are rounded to the 16 bits of the products, half a step, 2^-8 in bf16 and
+                // 2^-11 in fp16; their sum is taken before, in 32: see pack_p in sz_attn.cu)
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {

@@ -336,7 +336,12 @@ sz_status sz_encode_noalloc(sz_dtype dtype, const sz_plan_t *d_plan, const void 
  * Queries, keys, values and outputs are BF16; the cache is BF16 or E5M2.
  * Arithmetic is in 32 bits, rounded once to the type that is written (to
  * nearest, ties to even; beyond E5M2's range that is infinity, as in torch's
- * conversion).  The conventions at the top of this file hold here too; the
+ * conversion), but for the products of sz_attn_paged, whose factors have 16:
+ * a softmax weight is rounded to BF16 over a BF16 cache (by at most 2^-8 of it)
+ * and to fp16 over an E5M2 cache (2^-11) before it multiplies its value, while
+ * the sum that the row is divided by is that of the weights in 32 bits; and over
+ * an E5M2 cache a query element below 2^-30 of its head's largest is off by at
+ * most 2^-38 of that.  The conventions at the top of this file hold here too; the
  * structs below are host data, read during the call.  d_ws is sized by
  * sz_ops_workspace_bytes and zeroed once by sz_workspace_init.  It is the
  * operators' own: not to be used by the codec's calls too, whose layout of a
