@@ -2,6 +2,7 @@
 // (include/splitzip.h): host-side argument checks and dispatch.  No device
 // memory is allocated here.
 #include <cmath>
+#include <cstdlib>
 
 #include "sz_ops.cuh"
 
@@ -69,8 +70,24 @@ void extent(const sz_heads_t &h, uint64_t tokens, uint32_t dim, uintptr_t *a, ui
     *b = *a + 2 * ((tokens - 1) * h.token_stride + (uint64_t(h.heads) - 1) * h.head_stride + dim);
 }
 
+// Whether rows of two views of one layout meet, y's first being `gap` elements
+// behind x's: for some difference of heads and of tokens they are less than a
+// row apart.
+bool rows_meet(int64_t gap, int64_t token_stride, int64_t head_stride, int64_t tokens, int64_t x_heads, int64_t y_heads,
+               int64_t dim) {
+    for (int64_t h = 1 - x_heads; h < y_heads; ++h) {
+        const int64_t v = gap + h * head_stride;
+        int64_t t = tokens > 1 && token_stride > 0 ? -(v / token_stride) : 0;  // brings v nearest to 0, or next to that
+        t = t < 1 - tokens ? 1 - tokens : (t > tokens - 1 ? tokens - 1 : t);
+        for (int64_t u = t - 1; u <= t + 1; ++u)
+            if (u > -tokens && u < tokens && std::llabs(v + u * token_stride) < dim) return true;
+    }
+    return false;
+}
+
 // Whether two views' rows can meet: their extents do, and they are not the
 // interleaved columns of one buffer (heads [a, b) and [b, c) of each token).
+// Views of unlike layouts whose extents meet are taken to.
 bool may_overlap(const sz_heads_t &x, const sz_heads_t &y, uint64_t tokens, uint32_t dim) {
     if (tokens == 0) return false;
     uintptr_t a, b, c, d;
@@ -84,6 +101,11 @@ bool may_overlap(const sz_heads_t &x, const sz_heads_t &y, uint64_t tokens, uint
         const uint64_t gap = a <= c ? (c - a) % period : (period - (a - c) % period) % period;  // of y behind x
         if (wx <= period && wy <= period && gap >= wx && gap + wy <= period) return false;
     }
+    // (one token's or one head's stride is nothing)
+    if ((tokens == 1 || x.token_stride == y.token_stride) &&
+        (x.heads == 1 || y.heads == 1 || x.head_stride == y.head_stride))
+        return rows_meet((int64_t(c) - int64_t(a)) / 2, int64_t(x.token_stride),
+                         int64_t(x.heads > 1 ? x.head_stride : y.head_stride), int64_t(tokens), x.heads, y.heads, dim);
     return true;
 }
 
