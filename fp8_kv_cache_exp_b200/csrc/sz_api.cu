@@ -54,7 +54,7 @@ const char *sz_status_string(sz_status s) {
         case SZ_ERR_BUFFER_TOO_SMALL: return "buffer too small";
         case SZ_ERR_CORRUPT_STREAM: return "corrupt stream";
         case SZ_ERR_CUDA: return "CUDA runtime error";
-        case SZ_ERR_TIMEOUT: return "look-back wait timed out";
+        case SZ_ERR_TIMEOUT: return "a wait on the device took longer than its limit";
         case SZ_ERR_PLAN_MISMATCH: return "data or sizes do not match the plan";
         case SZ_ERR_INTERNAL: return "internal consistency check failed";
     }

@@ -34,7 +34,7 @@
 // scores have shorter chains, but q k' of 64 columns reads 6 KB of shared memory
 // in what would be 32 clocks, and takes 48.
 //
-// Keys and values come by tensor copies of 8 to 64 rows of a page, where pages
+// Keys and values come by tensor copies of 8 to 128 rows of a page, where pages
 // are a multiple of 8 tokens and all of the block is seen.  Other blocks, the
 // ends of what is seen among them, are fetched row by row by 16-byte
 // asynchronous copies, with zeros for places that nobody sees.  Both bring the

@@ -85,3 +85,7 @@ def test_descriptors_of_a_sequences_pages():
     for tokens in (65, -1):
         with pytest.raises(ValueError):
             c.pages(0, tokens)
+
+
+def test_a_timeout_is_not_only_the_codecs():
+    assert "look-back" not in sz.sz_status_string(sz.SZ_ERR_TIMEOUT) and "limit" in sz.sz_status_string(sz.SZ_ERR_TIMEOUT)
