@@ -7,8 +7,8 @@
 // is rounded to the type that v is multiplied in (bf16, or fp16 for an E5M2
 // cache).
 //
-// Measured: 64 sequences of up to 8192 places, 32 heads on 8 of 128: 237 us, 5.6
-// TB/s, 0.86 of a plain copy's rate; one sequence of 131,072 places, 32 heads on
+// Measured: 64 sequences of up to 8192 places, 32 heads on 8 of 128: 240 us, 5.5
+// TB/s, 0.85 of a plain copy's rate; one sequence of 131,072 places, 32 heads on
 // 4 in E5M2: 53 us, of which about 25 are fixed (the deal, the first pages' ids
 // and rows, the joining of 111 parts a head); one token over 777 places: 10 us,
 // all of it the latency of those steps.
@@ -567,6 +567,9 @@ sz_status run_dim(const AttnParams &p, int num_sms, cudaStream_t stream) {
     // Rows of a sequence and KV head, on average.  20 (8 sequences of 5 tokens, groups of 4,
     // 8192 places): 58 us here, 74 in tensor memory; 64 (4 of 16 tokens, 4096 places): 68 and 44;
     // one sequence of 16 tokens over 65,536: 232 and 82.  Wider heads' sums do not fit there twice.
+    // It is the average of the table's rows, all that the host knows: one long chunk among many
+    // rows of none or of one token goes the slow way (512 tokens over 4096 places: 53 us alone, 70
+    // in a table of 63 rows, 386 in one of 64).
     if (d <= 128 && rows > 32) return launch_attn_tc(p, DT, num_sms, stream);
     if (d <= 64) return rows <= 16 ? run<DT, 64, 1>(p, num_sms, stream) : run<DT, 64, 2>(p, num_sms, stream);
     if (d <= 128) return rows <= 16 ? run<DT, 128, 1>(p, num_sms, stream) : run<DT, 128, 2>(p, num_sms, stream);

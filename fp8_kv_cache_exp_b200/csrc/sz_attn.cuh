@@ -156,8 +156,13 @@ __device__ __forceinline__ bool work_whole(const AttnParams &p, Work &w, const u
 //
 // With `order`, tiles of at most kWholeMost blocks that are at least as many as
 // the CTAs are not cut: a part of a tile costs its queries, its results and their
-// joining, as much as three to four blocks, and cutting saves half a tile (two
-// 1024-token prompts of 32 heads of 80: 40 us whole, 48 cut).  (All
+// joining, as much as three to four blocks, and cutting saves half a tile.  Whole
+// and cut, on 148 CTAs: two 1024-token prompts of 32 heads of 80 (tiles of 2 to 8
+// blocks) 35 and 45 us; equal tiles of 8 blocks (64 tokens over 1024 places, 32
+// heads on 8 of 128), 152 of them 49 and 47, 192: 52 and 57, 240: 53 and 66; 152 of
+// 4 blocks 31 and 35.  A limit of 4 cuts the tiles of 8.  Longer tiles of prompts
+// would gain too: two of 1152 tokens 43 us whole, 54 as they are, of 2048 87 and 96;
+// of few equal long tiles a second round costs more than cutting them.  (All
 // threads call it then, and each has `order` behind the next barrier.)
 constexpr uint32_t kWholeMost = 8;
 template <int TR, int BN, int EXTRA>

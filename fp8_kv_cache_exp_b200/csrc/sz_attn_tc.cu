@@ -20,9 +20,10 @@
 // (through registers) when a row's maximum has grown by more, so that most
 // blocks leave them where they are.
 //
-// Measured: 2048 tokens over 8192 places, 32 heads on 8 of 128: 257 us, 0.94
-// PFLOP/s; two 1024-token prompts of 32 heads of 80: 40 us; five ragged chunks of
-// up to 700 tokens, window 1024, 32 heads on 4 in E5M2: 82 us.
+// Measured, with other inputs from call to call: 2048 tokens over 8192 places, 32
+// heads on 8 of 128: 263 us, 0.91 PFLOP/s; two 1024-token prompts of 32 heads of 80:
+// 39 us; five ragged chunks of up to 700 tokens, window 1024, 32 heads on 4 in
+// E5M2: 85 us.
 //
 // What bounds it: a block of 256 rows and heads of 128 is 2048 clocks of matrix
 // products and 2048 clocks of ex2 (16 a clock), if each tile's chain (scores,
@@ -71,8 +72,10 @@ constexpr uint64_t kLandLimitNs = 5000000ull;  // 5 ms
 constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;
 constexpr int kTcBlock = 128;
-// A tile's fixed costs in blocks: 0, 1, 2, 3, 4 took 48.2, 45.9, 46.0, 46.0 and
-// 49.5 us for two 1024-token prompts of 32 heads of 80.
+// A tile's fixed costs in blocks.  0, 1, 2, 3, 4 took, where tiles are cut: three
+// 2000-token prompts, 32 heads on 8 of 128: 164, 151, 142, 143, 144 us; four of 1500:
+// 136, 126, 123, 125, 126; 300 tokens over 4000 places: 61, 54, 53, 53, 53; 2048 over
+// 8192: 231, 227, 228, 228, 231.
 constexpr int kTcExtra = 2;
 constexpr uint32_t kFewParts = 4;             // a tile of so many parts is joined by the last of them
 constexpr uint32_t kQPanel = 128 * 128;       // bytes of 128 rows of 64 16-bit elements
@@ -991,9 +994,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
                 }
                 // The tiles take turns at ex2, three quarters of a block apart: side by
                 // side they would both wait for it, and then both for their products
-                // (2048-token chunk: 308 us; by turns 242).  A polynomial in place of a
-                // part of the ex2 made it 255: its multiply-adds, two to an instruction
-                // or not, take the issue slots.
+                // (2048 tokens over 8192 places, the same inputs again and again: 293 us, by
+                // turns 229; 263 with others each time, as at the top).  A polynomial in
+                // place of a part of the ex2 took 13 us more: its multiply-adds, two to an
+                // instruction or not, take the issue slots.
                 if (t.rows > 128) {
                     if ((i == 1 || turns > 0) && !warp_wait(&aux->turn[i], (turns - 1 + i) & 1, aux, p)) return;
                     ++turns;
