@@ -380,6 +380,18 @@ __device__ __forceinline__ Range seen_by_all(const AttnParams &p, const Part &t)
     return lo < hi ? Range{lo, hi} : Range{t.r.hi, t.r.hi};
 }
 
+// Blocks of a tile that hold edges: those before `lo` and from `hi` on.
+struct EdgeBlocks {
+    uint32_t lo, hi;
+    __device__ __forceinline__ bool has(uint32_t j) const { return j < lo || j >= hi; }
+};
+template <int BN>
+__device__ __forceinline__ EdgeBlocks edge_blocks(const AttnParams &p, const Part &t) {
+    const Range all = seen_by_all(p, t);
+    return EdgeBlocks{t.r.lo < all.lo ? (all.lo + BN - 1) / BN - t.block0 : 0,
+                      t.r.hi > all.hi ? all.hi / BN - t.block0 : 0xffffffffu};
+}
+
 // Whether some of [lo, hi), places of the tile, are edges.
 __device__ __forceinline__ bool has_edges(const Range &all, uint32_t lo, uint32_t hi) {
     return lo < hi && (lo < all.lo || hi > all.hi);

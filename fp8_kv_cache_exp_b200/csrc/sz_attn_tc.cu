@@ -350,23 +350,24 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
         const int32_t *ids = p.cache.table + uint64_t(w.seq) * p.cache.table_stride;
         const uint32_t part_hi = min((t.block0 + t.to) * kTcBlock, t.r.hi);
         const uint64_t head_off = uint64_t(w.head) * d * C::EB + piece * 16;
-        const Range all = seen_by_all(p, t);
-        // Whether block j has edges.
-        auto edges = [&](uint32_t j) {
-            const uint32_t at = (t.block0 + j) * kTcBlock;
-            return has_edges(all, max(at, t.r.lo), min(at + kTcBlock, part_hi));
-        };
-        auto is_edge = [&](uint32_t j, uint32_t row) {
-            const uint32_t at = (t.block0 + j) * kTcBlock + row;
-            return at < all.lo || at >= all.hi;
-        };
-        // The u-th piece of block j's edges that this thread has copied.
-        auto clean = [&](uint32_t j, uint32_t u, uint4 &v) {
-            if (is_edge(j, row0 + u * ROWS) && make_finite<DT>(v)) {
+        const EdgeBlocks edges = edge_blocks<kTcBlock>(p, t);
+        // Values of edges among the pieces of block j that this thread has copied, `from(u)` their
+        // addresses: those that are not finite become 0.
+        auto look = [&](uint32_t j, auto &&from) {
+            uint32_t c = 0;
+#pragma unroll 4
+            for (uint32_t u = 0; u < N; ++u) c |= carries<DT>(lds_u128(from(u)));
+            if ((c & kNotFinite<DT>) == 0) return;
+            const Range all = seen_by_all(p, t);
+#pragma unroll 1
+            for (uint32_t u = 0; u < N; ++u) {
+                const uint32_t at = (t.block0 + j) * kTcBlock + row0 + u * ROWS;
+                uint4 v = lds_u128(from(u));
+                if ((at >= all.lo && at < all.hi) || !make_finite<DT>(v)) continue;
+                sts_u128(from(u), v);
                 *reinterpret_cast<volatile uint32_t *>(&aux->edge) = 1;
-                return true;
             }
-            return false;
+            fence_proxy_async_smem();
         };
 
         // the place of this lane's row of a block, and its page's id
@@ -459,7 +460,7 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
                 for (uint32_t n = 0; n < tiles; ++n, ++issued) {
                     if (!wait_free(issued)) return;
                     // (the query warps look at edges)
-                    const bool edge = (n & 1) && edges(t.from + n / 2);
+                    const bool edge = (n & 1) && edges.has(t.from + n / 2);
                     next_fetch(n, base + C::RING_AT + (issued % C::STAGES) * C::STAGE, C::STAGE,
                                edge ? &aux->edge_here[issued % C::STAGES] : &aux->full[issued % C::STAGES]);
                 }
@@ -478,17 +479,16 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
                     if (!warp_wait(&aux->raw_full[slot], (x / C::RAWS) & 1, aux, p) || !wait_free(issued)) return;
                     if (has_piece) {
                         const uint32_t m = x - raw0, j = t.from + m / 2;
-                        const bool edge = (m & 1) && edges(j);
+                        if ((m & 1) && edges.has(j))
+                            look(j, [&](uint32_t u) {
+                                return base + C::RAW_AT + slot * C::RAW + (row0 + u * ROWS) * DP + piece * 16;
+                            });
 #pragma unroll
                         for (uint32_t u0 = 0; u0 < N; u0 += 4) {
                             uint4 v[4];
 #pragma unroll
                             for (uint32_t u = 0; u < 4; ++u)
                                 v[u] = lds_u128(base + C::RAW_AT + slot * C::RAW + (row0 + (u0 + u) * ROWS) * DP + piece * 16);
-                            if (edge) {
-#pragma unroll
-                                for (uint32_t u = 0; u < 4; ++u) clean(j, u0 + u, v[u]);
-                            }
 #pragma unroll
                             for (uint32_t u = 0; u < 4; ++u)
                                 spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + (u0 + u) * ROWS, piece, v[u]);
@@ -521,12 +521,7 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
             auto arrived = [&](uint32_t to) {
                 for (uint32_t x = ready; x < to; ++x) {
                     const uint32_t n = x - first;
-                    if (!(n & 1) || !has_piece || !edges(t.from + n / 2)) continue;
-#pragma unroll 1
-                    for (uint32_t u = 0; u < N; ++u) {
-                        uint4 v = lds_u128(at(x, u));
-                        if (clean(t.from + n / 2, u, v)) sts_u128(at(x, u), v);
-                    }
+                    if ((n & 1) && has_piece && edges.has(t.from + n / 2)) look(t.from + n / 2, [&](uint32_t u) { return at(x, u); });
                 }
                 hand_over(to);
             };
@@ -552,18 +547,15 @@ __device__ __forceinline__ void load_parts(const AttnParams &p, const Maps &maps
                 if (n < LAG) continue;
                 const uint32_t m = n - LAG;  // the tile that has come
                 cp_wait<LAG>();
-                const bool edge = (m & 1) && edges(t.from + m / 2);
                 if (!wait_free(issued)) return;
                 if (has_piece) {
+                    if ((m & 1) && edges.has(t.from + m / 2))
+                        look(t.from + m / 2, [&](uint32_t u) { return raw + (m % C::RAWS) * C::RAW + u * 2048; });
 #pragma unroll
                     for (uint32_t u0 = 0; u0 < N; u0 += 4) {
                         uint4 v[4];
 #pragma unroll
                         for (uint32_t u = 0; u < 4; ++u) v[u] = lds_u128(raw + (m % C::RAWS) * C::RAW + (u0 + u) * 2048);
-                        if (edge) {
-#pragma unroll
-                            for (uint32_t u = 0; u < 4; ++u) clean(t.from + m / 2, u0 + u, v[u]);
-                        }
 #pragma unroll
                         for (uint32_t u = 0; u < 4; ++u)
                             spread16(base + C::RING_AT + (issued % C::STAGES) * C::STAGE, row0 + (u0 + u) * ROWS, piece, v[u]);
@@ -597,7 +589,7 @@ __device__ __forceinline__ void load_role(const AttnParams &p, const Maps &maps,
 // queries the warps look at the values of its edges, where these come by tensor
 // copies in the products' layout (`edges`): nobody has had those in registers.
 // (Two 1024-token prompts of 32 heads of 80, and 2048 tokens over 8192 places:
-// 39 and 227 us; by the load warps 43 and 265; by one warp beside the queries 47
+// 39 and 224 us; by the load warps 43 and 265; by one warp beside the queries 47
 // and 228; not at all 36 and 223.)
 constexpr uint32_t kQueryWarps = 2;
 template <int DT, int DP>
@@ -662,9 +654,13 @@ __device__ __forceinline__ void query_parts(const AttnParams &p, const CUtensorM
         }
         if (DT == SZ_BF16 && edges) {
             const Range all = seen_by_all(p, t);
+            const EdgeBlocks blocks = edge_blocks<kTcBlock>(p, t);
             for (uint32_t j = t.from; j < t.to; ++j) {
+                if (!blocks.has(j)) {  // on to the ones at the other end
+                    j = min(blocks.hi, t.to) - 1;
+                    continue;
+                }
                 const uint32_t at = (t.block0 + j) * kTcBlock, lo = max(at, t.r.lo), hi = min(at + kTcBlock, t.r.hi);
-                if (!has_edges(all, lo, hi)) continue;
                 const uint32_t stage = (kv + 2 * (j - t.from) + 1) % C::STAGES;
                 if (!warp_wait(&aux->edge_here[stage], (edge_phases >> stage) & 1, aux, p)) return;
                 edge_phases ^= 1u << stage;
