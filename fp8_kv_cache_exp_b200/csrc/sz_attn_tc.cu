@@ -21,9 +21,9 @@
 // blocks leave them where they are.
 //
 // Measured, with other inputs from call to call: 2048 tokens over 8192 places, 32
-// heads on 8 of 128: 263 us, 0.91 PFLOP/s; two 1024-token prompts of 32 heads of 80:
-// 39 us; five ragged chunks of up to 700 tokens, window 1024, 32 heads on 4 in
-// E5M2: 85 us.
+// heads on 8 of 128: 260 us, 0.92 PFLOP/s; two 1024-token prompts of 32 heads of 80:
+// 40 us; five ragged chunks of up to 700 tokens, window 1024, 32 heads on 4 in
+// E5M2: 82 us.
 //
 // What bounds it: a block of 256 rows and heads of 128 is 2048 clocks of matrix
 // products and 2048 clocks of ex2 (16 a clock), if each tile's chain (scores,
@@ -991,7 +991,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Work w, uint32
                 // The tiles take turns at ex2, three quarters of a block apart: side by
                 // side they would both wait for it, and then both for their products
                 // (2048 tokens over 8192 places, the same inputs again and again: 293 us, by
-                // turns 229; 263 with others each time, as at the top).  A polynomial in
+                // turns 229; with others each time, as at the top, the clocks are lower).  A polynomial in
                 // place of a part of the ex2 took 13 us more: its multiply-adds, two to an
                 // instruction or not, take the issue slots.
                 if (t.rows > 128) {
