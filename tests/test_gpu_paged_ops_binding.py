@@ -1,5 +1,6 @@
 """The Python binding of the operators on a paged cache on the GPU: threads and streams."""
 import ctypes
+import gc
 import threading
 import time
 
@@ -54,6 +55,8 @@ def test_a_workspace_zeroed_on_another_stream(operators):
     ns = [1 << 24] * 4
     s = torch.cuda.Stream()
     n = m.sz_ops_workspace_bytes(cache) if operators else m.sz_workspace_bytes_batched(m.SZ_BF16, ns)
+    gc.collect()
+    torch.cuda.empty_cache()                         # (no other block of this size to hand out)
     old = torch.empty(n, dtype=torch.uint8, device="cuda")
     address = old.data_ptr()
     old.fill_(1), m.new_ops_workspace(stream=s)      # (first calls wait for the device)
